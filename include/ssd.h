@@ -54,7 +54,8 @@ typedef enum {
     SSD_ERR_INVALID_ARG = 1,   /* null/misaligned pointer, negative size, inconsistent dims */
     SSD_ERR_UNSUPPORTED = 2,   /* valid but outside the supported geometry (fail closed) */
     SSD_ERR_CUDA = 3,          /* a CUDA runtime call failed (message in ssd_last_error) */
-    SSD_ERR_TIMEOUT = 4        /* a device-side bounded wait expired */
+    SSD_ERR_TIMEOUT = 4,       /* a device-side bounded wait expired */
+    SSD_ERR_NO_PAGES = 5       /* a page pool has too few free pages for the request */
 } ssd_status;
 
 typedef enum {
@@ -311,10 +312,149 @@ ssd_status ssd_strict_state_update(const ssd_chunk_cache* cache, const void* x, 
                                    const float* D, void* y, const ssd_dims* dims, int chunk, ssd_stream_t stream);
 
 /*
+ * Linear attention with a decay for each head, the mixer of hybrid stacks whose state
+ * update does not depend on the data. For every sequence and key/value head g, with
+ * lam = exp(log_decay[g]) and R = H / Hk query heads h = g*R .. g*R+R-1 sharing g:
+ *
+ *     S_t    = lam * S_{t-1} + v_t k_t^T          (FP32 state, stored [V][K], K contiguous)
+ *     o_t[h] = scale * S_t q_t[h]
+ *
+ * Layouts (T tokens in the call, packed like the scan's inputs):
+ *   q [T,H,K], k [T,Hk,K], v [T,Hk,V] in `dtype`; heads contiguous, tokens q_stride,
+ *     k_stride and v_stride elements apart (0: contiguous), so q, k and v may be slices of
+ *     one projection's output; every sequence of a dense batch follows the previous one
+ *     without a gap, seqlen strides on;
+ *   o [T,H,V] in `dtype`, contiguous;  log_decay [Hk] float32, <= 0 and finite (0: no decay);
+ *   states [nseq,Hk,V,K] float32, or [n_pages,Hk,V,K] with a page list.
+ * A page list ([nseq] int32, device) gives each sequence's state's place in a pool of
+ * n_pages states. -1 stands for none: a zero initial state, a final state that is not
+ * written, a decode row that is skipped (its o row is left as it is). A page outside the
+ * pool latches SSD_ERR_INVALID_ARG and counts as none.
+ * Supported: K and V multiples of 8 up to 128; H a multiple of Hk; q, k, v, o and states
+ * 16-byte aligned, strides a multiple of 16 bytes.
+ */
+typedef struct {
+    int64_t batch;             /* dense: batch sequences of seqlen tokens (decode: seqlen 1) */
+    int64_t seqlen;
+    int32_t nseq;              /* packed: nseq sequences, total_tokens rows */
+    int64_t total_tokens;
+    int32_t nheads;            /* H */
+    int32_t nkvheads;          /* Hk */
+    int32_t headdim_k;         /* K */
+    int32_t headdim_v;         /* V */
+    int64_t q_stride;
+    int64_t k_stride;
+    int64_t v_stride;
+    int64_t n_pages;           /* states in the pool(s); read only with a page list */
+    ssd_dtype dtype;
+    void* workspace;           /* prompts: as in ssd_dims; decode needs none */
+    size_t workspace_bytes;
+} ssd_linear_attn_dims;
+
+/* Bytes of device scratch ssd_linear_attn_fwd needs (as ssd_scan_fwd_workspace_size). */
+ssd_status ssd_linear_attn_fwd_workspace_size(const ssd_linear_attn_dims* dims, size_t* bytes);
+
+/*
+ * Prompts: the chunked form over every sequence of the call (dense batch, or packed with
+ * cu_seqlens [nseq+1] as in ssd_scan_fwd).
+ *   init_state: states the sequences start from, or NULL for zero; init_pages: page list
+ *     for it, or NULL (state s belongs to sequence s).
+ *   final_state: output, the states after each sequence's last token (the initial state
+ *     for an empty sequence), or NULL; final_pages: page list for it, or NULL.
+ *   init_state and final_state may be the same array (states continue in place); they must
+ *   not overlap otherwise. With a page list, a final page that an earlier sequence writes,
+ *   or that another sequence starts from (one array), is not written and latches
+ *   SSD_ERR_INVALID_ARG. With page lists both arrays have n_pages states.
+ *   scale: usually 1 / sqrt(K).
+ * A NaN or infinity in k or v reaches every output of its sequence and key/value head from
+ * the start of its 128-token chunk on (the chunk's products are dense); one in q reaches its
+ * own token's outputs only. Other sequences never see it.
+ */
+ssd_status ssd_linear_attn_fwd(const void* q, const void* k, const void* v, const float* log_decay, float scale,
+                               const float* init_state, const int32_t* init_pages, const int32_t* cu_seqlens,
+                               void* o, float* final_state, const int32_t* final_pages,
+                               const ssd_linear_attn_dims* dims, ssd_stream_t stream);
+
+/*
+ * Single tokens: the recurrent form for one token of each of dims->batch rows (seqlen 1),
+ * states updated in place. q [batch,H,K], k [batch,Hk,K], v [batch,Hk,V], o [batch,H,V].
+ *   pages: each row's state in a pool of n_pages, -1 for a padded row; NULL: state b
+ *     belongs to row b. A page named by two rows is updated for the first of them only; the
+ *     others are left as they are and latch SSD_ERR_INVALID_ARG.
+ */
+ssd_status ssd_linear_attn_update(float* state, const void* q, const void* k, const void* v, const float* log_decay,
+                                  float scale, const int32_t* pages, void* o, const ssd_linear_attn_dims* dims,
+                                  ssd_stream_t stream);
+
+/*
+ * Pages of a state cache. A pool is a set of device arrays with the same number of pages
+ * along their first dimension (page p of array i: page_bytes[i] bytes at arrays[i] +
+ * p * page_bytes[i]); one page is one state in every array, for instance the SSM state,
+ * conv state and linear attention state of every layer. Metadata, all int32 on the device
+ * and all zero / -1 for an empty pool (refcount 0, table -1, length 0, live -1):
+ *   refcount [n_pages]: rows that hold the page, 0 for a free one;
+ *   table [n_rows, max_pages]: the pages of each row (one sequence) in order, -1 past them;
+ *   length [n_rows]: pages of the row;
+ *   live [n_rows]: the row's last page, the only one its next tokens change, or -1. It is a
+ *     page list for ssd_linear_attn_update and ssd_linear_attn_fwd as it stands.
+ * A row's earlier pages are snapshots that other rows may share.
+ *
+ * Every call is two launches on `stream` and never waits for the device; lists are int32
+ * device arrays, an entry of -1 in them is skipped. A request is checked as a whole before
+ * anything changes: an index out of range, a row or page named twice, a table entry that
+ * holds no page in use latches SSD_ERR_INVALID_ARG, and too few free pages latch
+ * SSD_ERR_NO_PAGES; either way the call changes nothing. New pages are the lowest free ones,
+ * in the order of the request. Calls on one pool must not overlap on the device.
+ */
+typedef struct {
+    int32_t n_pages;           /* 1 .. 2^20 */
+    int32_t n_rows;            /* 1 .. 2^20 */
+    int32_t max_pages;         /* per row */
+    int32_t n_arrays;          /* 0 .. 128 */
+    void* const* arrays;       /* host array of device pointers */
+    const int64_t* page_bytes; /* host array, > 0; any alignment (multiples of 16 are fast) */
+    int32_t* refcount;
+    int32_t* table;
+    int32_t* length;
+    int32_t* live;
+    void* workspace;           /* ssd_pages_workspace_size bytes, or NULL (as in ssd_dims) */
+    size_t workspace_bytes;
+} ssd_page_pool;
+
+/* Bytes of device scratch of a call on `pool` with n list entries. */
+ssd_status ssd_pages_workspace_size(const ssd_page_pool* pool, int32_t n, size_t* bytes);
+
+/* One more page at the end of each listed row (its new live page). copy_last != 0: it starts
+ * as a copy of the row's last page, which thereby becomes a snapshot; else, and for a row
+ * without pages, its contents are left as they are. A full row is an invalid request. */
+ssd_status ssd_pages_append(const ssd_page_pool* pool, const int32_t* rows, int32_t n, int copy_last,
+                            ssd_stream_t stream);
+
+/* children[i] (empty rows) continue parents[i]: earlier pages are shared, the live page is
+ * copied into a new one. A parent may have several children; no child may be a parent. */
+ssd_status ssd_pages_fork(const ssd_page_pool* pool, const int32_t* parents, const int32_t* children, int32_t n,
+                          ssd_stream_t stream);
+
+/* The listed rows become empty; pages that no other row holds become free. One launch. */
+ssd_status ssd_pages_free(const ssd_page_pool* pool, const int32_t* rows, int32_t n, ssd_stream_t stream);
+
+/* Pages in use move to the front of the pool: those past the new end go, in ascending order,
+ * into the free pages before it, and the table and live pages follow. remap [n_pages] int32:
+ * each page's new number, -1 for a free one. counts [2] int32: pages in use, pages moved. */
+ssd_status ssd_pages_compact(const ssd_page_pool* pool, int32_t* remap, int32_t* counts, ssd_stream_t stream);
+
+/* The bytes of pages src[i] into pages dst[i], whatever the metadata say (restoring a
+ * snapshot into a live page, for instance). The dst pages are all different and none is
+ * another pair's src. */
+ssd_status ssd_pages_copy(const ssd_page_pool* pool, const int32_t* src, const int32_t* dst, int32_t n,
+                          ssd_stream_t stream);
+
+/*
  * Waits for `stream`, then reads and clears the device error word: SSD_OK, or the
  * first error a kernel latched since the last read (SSD_ERR_INVALID_ARG for bad
- * cu_seqlens or A > 0, SSD_ERR_TIMEOUT for an expired bounded wait). SSD_ERR_CUDA
- * if the wait itself failed.
+ * cu_seqlens, A > 0 or a bad page request, SSD_ERR_TIMEOUT for an expired bounded wait,
+ * SSD_ERR_NO_PAGES for a page request beyond the pool). SSD_ERR_CUDA if the wait itself
+ * failed.
  */
 ssd_status ssd_get_device_status(ssd_stream_t stream);
 

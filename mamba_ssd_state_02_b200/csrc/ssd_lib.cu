@@ -23,6 +23,8 @@
 #include "ssd_conv.cuh"
 #include "ssd_norm.cuh"
 #include "ssd_decode.cuh"
+#include "ssd_linattn.cuh"
+#include "ssd_pages.cuh"
 #include "ssd_scan_simt.cuh"
 #include "ssd_strict.cuh"
 #include "ssd_scan_tc.cuh"
@@ -52,13 +54,15 @@ ssd_status cuda_fail(cudaError_t e, const char* what) {
 // Per-kernel event timing (ssd_profile_enable / ssd_profile_read).
 enum Stage { ST_TABLE, ST_CUMSUM, ST_CHUNK_STATE, ST_STATE_PASSING, ST_CHUNK_SCAN, ST_STATE_UPDATE,
              ST_CONV, ST_CONV_UPDATE, ST_NORM, ST_STRICT_CUMSUM, ST_STRICT_STATE, ST_STRICT_PASSING,
-             ST_STRICT_SCAN, ST_STRICT_CACHE, ST_STRICT_UPDATE, ST_STRICT_FOLD, ST_COUNT };
+             ST_STRICT_SCAN, ST_STRICT_CACHE, ST_STRICT_UPDATE, ST_STRICT_FOLD, ST_LA_STATE, ST_LA_SCAN, ST_LA_UPDATE,
+             ST_PAGES_PLAN, ST_PAGES_MOVE, ST_COUNT };
 const char* const kStageName[ST_COUNT] = {"ssd_chunk_table", "ssd_chunk_cumsum", "ssd_chunk_state",
                                           "ssd_state_passing", "ssd_chunk_scan", "ssd_state_update", "ssd_conv1d", "ssd_conv1d_update",
                                           "ssd_gated_rmsnorm", "ssd_strict_cumsum", "ssd_strict_chunk_state",
                                           "ssd_strict_state_passing", "ssd_strict_chunk_scan",
                                           "ssd_strict_cache_fill", "ssd_strict_state_update",
-                                          "ssd_strict_fold"};
+                                          "ssd_strict_fold", "ssd_linear_attn_state", "ssd_linear_attn_scan",
+                                          "ssd_linear_attn_update", "ssd_pages_plan", "ssd_pages_move"};
 constexpr size_t kMaxRecords = 65536;
 
 struct Profiler {
@@ -680,7 +684,8 @@ ssd_status ssd_get_device_status(ssd_stream_t stream) {
         return SSD_OK;
     }
     if (code == SSD_ERR_TIMEOUT) return fail(SSD_ERR_TIMEOUT, "a device-side bounded wait expired");
-    return fail((ssd_status)code, "a kernel rejected its data (bad cu_seqlens, or A > 0 / not finite)");
+    if (code == SSD_ERR_NO_PAGES) return fail(SSD_ERR_NO_PAGES, "a page pool has too few free pages for the request");
+    return fail((ssd_status)code, "a kernel rejected its data (bad cu_seqlens or pages, or A or log_decay > 0 / not finite)");
 }
 
 const char* ssd_last_error(void) { return t_last_error.c_str(); }
@@ -1301,4 +1306,487 @@ extern "C" ssd_status ssd_strict_state_update(const ssd_chunk_cache* cache, cons
     t_launches = 2;
     t_last_error.clear();
     return SSD_OK;
+}
+
+// ---------------------------------------------------------------------------------
+// Linear attention with a decay for each head: prompts and single tokens.
+namespace ssd {
+namespace {
+
+struct LaPlan {
+    la::Args a{};
+    int64_t T = 0, max_segs = 0;
+    bool bf16 = false, varlen = false;
+    size_t off_table = 0, off_first = 0, off_count = 0, off_order = 0, off_slots = 0, bytes = 0;
+};
+
+// Segment length in tokens (a multiple of 128). A pass's CTAs, one per (segment, key/value
+// head, 64 columns of V), run in waves of one per SM; a CTA costs its chunks plus about two
+// chunks of prologue and epilogue. More than one segment per sequence adds the state pass
+// (about half a chunk's cost per chunk, R query heads being nothing to it) and its launch
+// (about two chunks). Dense: the number of segments per sequence with the least cost.
+// Packed (lengths known on the device only): the same with the mean length, where the
+// longest segments are what the last wave waits for.
+int la_segment_tokens(const LaPlan& p) {
+    constexpr int64_t kC = 128;
+    const la::Args& a = p.a;
+    if (const int v = g_segment_override.load()) return v;
+    const int64_t nsm = sm_count(), heads = (int64_t)a.Hk * ((a.V + 63) / 64);
+    if (!p.varlen) {
+        const int64_t nch = std::max<int64_t>(1, (a.seqlen + kC - 1) / kC);
+        double best = 0;
+        int64_t ls = nch;
+        for (int64_t n = 1; n <= std::min<int64_t>(nch, 64); ++n) {
+            const int64_t m = (nch + n - 1) / n, segs = (nch + m - 1) / m;
+            auto waves = [&](int64_t s) { return (double)((a.nseq * s * heads + nsm - 1) / nsm); };
+            double c = waves(segs) * (double)(m * a.R + 2);
+            if (segs > 1) c += waves(segs - 1) * (0.5 * (double)m + 2) + 2;
+            if (n == 1 || c < best) {
+                best = c;
+                ls = m;
+            }
+        }
+        return (int)std::min<int64_t>(ls * kC, 1 << 20);
+    }
+    const double chunks = (double)p.T / kC + 0.5 * a.nseq, mean = chunks / std::max(1, a.nseq), U = chunks * heads / nsm;
+    double best = 0;
+    int64_t ls = 2;
+    for (int64_t m = 2; m <= 8192; m *= 2) {
+        const double frac = std::max(0.0, 1.0 - (double)m / (2 * mean));
+        const double c = U * a.R + (double)(std::min<double>(m, 2 * mean) * a.R) + 0.5 * (U * frac + (frac > 0 ? m : 0)) +
+                         2 * U / std::min<double>(m, mean) + (frac > 0 ? 4 : 0);
+        if (m == 2 || c < best) {
+            best = c;
+            ls = m;
+        }
+    }
+    return (int)(ls * kC);
+}
+
+ssd_status la_check(const ssd_linear_attn_dims* d, bool varlen, LaPlan* out) {
+    if (!d) return fail(SSD_ERR_INVALID_ARG, "dims is NULL");
+    if (d->nheads <= 0 || d->nkvheads <= 0 || d->headdim_k <= 0 || d->headdim_v <= 0)
+        return fail(SSD_ERR_INVALID_ARG, "nheads, nkvheads, headdim_k and headdim_v must be positive");
+    if (d->nheads % d->nkvheads != 0)
+        return fail(SSD_ERR_UNSUPPORTED, "nheads (%d) must be a multiple of nkvheads (%d)", d->nheads, d->nkvheads);
+    if (d->headdim_k % 8 || d->headdim_k > 128 || d->headdim_v % 8 || d->headdim_v > 128)
+        return fail(SSD_ERR_UNSUPPORTED, "headdim_k (%d) and headdim_v (%d) must be multiples of 8 up to 128", d->headdim_k,
+                    d->headdim_v);
+    if (d->dtype != SSD_DTYPE_F32 && d->dtype != SSD_DTYPE_BF16)
+        return fail(SSD_ERR_INVALID_ARG, "unknown dtype %d", (int)d->dtype);
+    if (d->nheads > 65535) return fail(SSD_ERR_UNSUPPORTED, "more than 65535 heads");
+    LaPlan p;
+    la::Args& a = p.a;
+    p.bf16 = d->dtype == SSD_DTYPE_BF16;
+    p.varlen = varlen;
+    a.H = d->nheads;
+    a.Hk = d->nkvheads;
+    a.R = a.H / a.Hk;
+    a.K = d->headdim_k;
+    a.V = d->headdim_v;
+    const int64_t unit = p.bf16 ? 8 : 4;
+    struct { int64_t given, least; int64_t* to; const char* name; } st[] = {
+        {d->q_stride, (int64_t)a.H * a.K, &a.q_stride, "q_stride"},
+        {d->k_stride, (int64_t)a.Hk * a.K, &a.k_stride, "k_stride"},
+        {d->v_stride, (int64_t)a.Hk * a.V, &a.v_stride, "v_stride"}};
+    for (auto& s : st) {
+        *s.to = s.given ? s.given : s.least;
+        if (*s.to < s.least) return fail(SSD_ERR_INVALID_ARG, "%s is smaller than a token's heads", s.name);
+        if (*s.to % unit) return fail(SSD_ERR_UNSUPPORTED, "%s must be a multiple of 16 bytes", s.name);
+        if (*s.to >= (int64_t)1 << 31) return fail(SSD_ERR_UNSUPPORTED, "%s is 2^31 elements or more", s.name);
+    }
+    if (varlen) {
+        if (d->nseq < 0 || d->total_tokens < 0) return fail(SSD_ERR_INVALID_ARG, "nseq and total_tokens must be >= 0");
+        a.nseq = d->nseq;
+        p.T = d->total_tokens;
+    } else {
+        if (d->batch < 0 || d->seqlen < 0) return fail(SSD_ERR_INVALID_ARG, "batch and seqlen must be >= 0");
+        if (d->batch > INT32_MAX) return fail(SSD_ERR_UNSUPPORTED, "batch too large");
+        if (d->seqlen > 0 && d->batch > INT64_MAX / d->seqlen) return fail(SSD_ERR_INVALID_ARG, "batch*seqlen overflows");
+        a.nseq = (int32_t)d->batch;
+        a.seqlen = d->seqlen;
+        p.T = d->batch * d->seqlen;
+    }
+    if (p.T >= INT32_MAX) return fail(SSD_ERR_UNSUPPORTED, "more than 2^31-1 tokens in one call");
+    a.npages = d->n_pages;
+    *out = p;
+    return SSD_OK;
+}
+
+// Segments and the carving of the workspace.
+ssd_status la_plan(const ssd_linear_attn_dims* d, bool varlen, LaPlan* out) {
+    const ssd_status st = la_check(d, varlen, out);
+    if (st != SSD_OK) return st;
+    LaPlan& p = *out;
+    la::Args& a = p.a;
+    a.Ls = la_segment_tokens(p);
+    a.nps = varlen ? 0 : (int32_t)std::max<int64_t>(1, (a.seqlen + a.Ls - 1) / a.Ls);
+    p.max_segs = varlen ? p.T / a.Ls + a.nseq : (int64_t)a.nseq * a.nps;
+    if (p.max_segs * a.Hk * ((a.V + 63) / 64) >= INT32_MAX) return fail(SSD_ERR_UNSUPPORTED, "too many segments in one call");
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = off;
+        off = align_up(off + bytes, 256);
+        return o;
+    };
+    if (varlen) {
+        const size_t n = (size_t)std::max<int64_t>(1, p.max_segs);
+        p.off_table = take(sizeof(ChunkEntry) * n);
+        p.off_first = take(sizeof(int32_t) * ((size_t)a.nseq + 1));
+        p.off_count = take(sizeof(int32_t));
+        p.off_order = take(sizeof(int32_t) * n);
+    }
+    // Without a second segment anywhere no slot is used.
+    if (varlen ? p.T > a.Ls : a.nps > 1) p.off_slots = take(sizeof(float) * (size_t)p.max_segs * a.Hk * a.V * a.K);
+    p.bytes = std::max<size_t>(off, 256);
+    return SSD_OK;
+}
+
+template <typename T, bool OUT>
+ssd_status launch_la_simt(const LaPlan& p, int64_t segs, cudaStream_t st) {
+    const size_t smem = la::simt_smem(p.a.K, OUT);
+    cudaError_t e = cudaFuncSetAttribute(la::k_la_simt<T, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(linear attention)");
+    const int nvb = (p.a.V + la::kSimtV - 1) / la::kSimtV;
+    StageScope sc(OUT ? ST_LA_SCAN : ST_LA_STATE, st);
+    la::k_la_simt<T, OUT><<<(unsigned)(segs * p.a.Hk * nvb), la::kSimtThreads, smem, st>>>(p.a);
+    return SSD_OK;
+}
+
+template <typename T, int LPR>
+void launch_la_update(const LaPlan& p, float* state, const int32_t* pages, int64_t batch, cudaStream_t st) {
+    const la::Args& a = p.a;
+    constexpr int rows = la::kTokRows * (32 / LPR) * (la::kTokThreads / 32);
+    const int nvs = (a.V + rows - 1) / rows;
+    StageScope sc(ST_LA_UPDATE, st);
+    la::k_la_update<T, LPR><<<(unsigned)(batch * a.Hk * nvs), la::kTokThreads, 0, st>>>(
+        state, (const T*)a.q, (const T*)a.k, (const T*)a.v, a.log_decay, a.scale, pages, a.npages, (T*)a.o, nvs, a.Hk, a.R,
+        a.K, a.V, a.q_stride, a.k_stride, a.v_stride);
+}
+
+template <typename T>
+void dispatch_la_update(const LaPlan& p, float* state, const int32_t* pages, int64_t batch, cudaStream_t st) {
+    if (p.a.K <= 16) launch_la_update<T, 4>(p, state, pages, batch, st);
+    else if (p.a.K <= 32) launch_la_update<T, 8>(p, state, pages, batch, st);
+    else if (p.a.K <= 64) launch_la_update<T, 16>(p, state, pages, batch, st);
+    else launch_la_update<T, 32>(p, state, pages, batch, st);
+}
+
+}  // namespace
+}  // namespace ssd
+
+extern "C" ssd_status ssd_linear_attn_fwd_workspace_size(const ssd_linear_attn_dims* dims, size_t* bytes) {
+    if (!bytes) return fail(SSD_ERR_INVALID_ARG, "bytes is NULL");
+    LaPlan dense, packed;
+    const ssd_status sd = la_plan(dims, false, &dense), sp = la_plan(dims, true, &packed);
+    if (sd != SSD_OK && sp != SSD_OK) return sd;
+    *bytes = std::max(sd == SSD_OK ? dense.bytes : 0, sp == SSD_OK ? packed.bytes : 0);
+    t_last_error.clear();
+    return SSD_OK;
+}
+
+extern "C" ssd_status ssd_linear_attn_fwd(const void* q, const void* k, const void* v, const float* log_decay, float scale,
+                                          const float* init_state, const int32_t* init_pages, const int32_t* cu_seqlens,
+                                          void* o, float* final_state, const int32_t* final_pages,
+                                          const ssd_linear_attn_dims* dims, ssd_stream_t stream) {
+    LaPlan p;
+    ssd_status s = la_plan(dims, cu_seqlens != nullptr, &p);
+    if (s != SSD_OK) return s;
+    la::Args& a = p.a;
+    if (!log_decay) return fail(SSD_ERR_INVALID_ARG, "log_decay must be non-NULL");
+    if (p.T > 0 && (!q || !k || !v || !o)) return fail(SSD_ERR_INVALID_ARG, "q, k, v and o must be non-NULL");
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(init_state, 16) ||
+        !aligned(final_state, 16))
+        return fail(SSD_ERR_INVALID_ARG, "q, k, v, o and states must be 16-byte aligned");
+    if (!aligned(log_decay, 4) || !aligned(init_pages, 4) || !aligned(final_pages, 4) || !aligned(cu_seqlens, 4))
+        return fail(SSD_ERR_INVALID_ARG, "log_decay, page lists and cu_seqlens must be 4-byte aligned");
+    if ((init_pages && !init_state) || (final_pages && !final_state))
+        return fail(SSD_ERR_INVALID_ARG, "a page list without its states");
+    if ((init_pages || final_pages) && (dims->n_pages < 1 || dims->n_pages > INT32_MAX))
+        return fail(SSD_ERR_INVALID_ARG, "n_pages must be 1 .. 2^31-1 with a page list");
+    if (a.nseq == 0) {
+        t_launches = 0;
+        t_last_error.clear();
+        return SSD_OK;
+    }
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const bool two_pass = cu_seqlens ? p.T > a.Ls : a.nps > 1;
+    char* ws = static_cast<char*>(dims->workspace);
+    bool owned = false;
+    if (ws) {
+        if (dims->workspace_bytes < p.bytes)
+            return fail(SSD_ERR_INVALID_ARG, "workspace_bytes %zu < required %zu", dims->workspace_bytes, p.bytes);
+        if (!aligned(ws, 256)) return fail(SSD_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    } else if (cu_seqlens || two_pass) {
+        cudaError_t e = cudaMallocAsync(reinterpret_cast<void**>(&ws), p.bytes, st);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaMallocAsync(workspace)");
+        owned = true;
+    }
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.log_decay = log_decay;
+    a.scale = scale;
+    a.init = init_state;
+    a.init_pages = init_pages;
+    a.fin = final_state;
+    a.fin_pages = final_pages;
+    a.o = o;
+    a.slots = reinterpret_cast<float*>(ws + p.off_slots);
+    int n = 0;
+    if (cu_seqlens) {
+        auto* table = reinterpret_cast<ChunkEntry*>(ws + p.off_table);
+        auto* first = reinterpret_cast<int32_t*>(ws + p.off_first);
+        auto* count = reinterpret_cast<int32_t*>(ws + p.off_count);
+        auto* order = reinterpret_cast<int32_t*>(ws + p.off_order);
+        a.table = table;
+        a.first = first;
+        a.count = count;
+        a.order = order;
+        StageScope sc(ST_TABLE, st);
+        k_chunk_table<<<1, kTableThreads, 0, st>>>(cu_seqlens, a.nseq, p.T, 0, a.Ls, table, first, count, 0, nullptr, order,
+                                                   nullptr, nullptr, true);
+        ++n;
+    }
+    if (two_pass) {
+        const int64_t segs = cu_seqlens ? p.max_segs : (int64_t)a.nseq * (a.nps - 1);
+        s = p.bf16 ? launch_la_simt<__nv_bfloat16, false>(p, segs, st) : launch_la_simt<float, false>(p, segs, st);
+        ++n;
+    }
+    if (s == SSD_OK) {
+        s = p.bf16 ? launch_la_simt<__nv_bfloat16, true>(p, p.max_segs, st) : launch_la_simt<float, true>(p, p.max_segs, st);
+        ++n;
+    }
+    cudaError_t e = cudaGetLastError();
+    if (owned) {
+        const cudaError_t f = cudaFreeAsync(ws, st);
+        if (e == cudaSuccess) e = f;
+    }
+    if (s != SSD_OK) return s;
+    if (e != cudaSuccess) return cuda_fail(e, "kernel launch (linear attention)");
+    t_launches = n;
+    t_last_error.clear();
+    return SSD_OK;
+}
+
+extern "C" ssd_status ssd_linear_attn_update(float* state, const void* q, const void* k, const void* v,
+                                             const float* log_decay, float scale, const int32_t* pages, void* o,
+                                             const ssd_linear_attn_dims* dims, ssd_stream_t stream) {
+    if (!dims) return fail(SSD_ERR_INVALID_ARG, "dims is NULL");
+    if (dims->seqlen != 1) return fail(SSD_ERR_INVALID_ARG, "decode takes seqlen == 1 (got %lld)", (long long)dims->seqlen);
+    LaPlan p;
+    const ssd_status s = la_check(dims, false, &p);
+    if (s != SSD_OK) return s;
+    la::Args& a = p.a;
+    if (a.nseq == 0) {
+        t_launches = 0;
+        t_last_error.clear();
+        return SSD_OK;
+    }
+    if (!state || !q || !k || !v || !log_decay || !o) return fail(SSD_ERR_INVALID_ARG, "all decode pointers must be non-NULL");
+    if (!aligned(state, 16) || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16))
+        return fail(SSD_ERR_INVALID_ARG, "state, q, k, v and o must be 16-byte aligned");
+    if (!aligned(log_decay, 4) || !aligned(pages, 4))
+        return fail(SSD_ERR_INVALID_ARG, "log_decay and pages must be 4-byte aligned");
+    if (pages && (dims->n_pages < 1 || dims->n_pages > INT32_MAX))
+        return fail(SSD_ERR_INVALID_ARG, "n_pages must be 1 .. 2^31-1 with a page list");
+    if ((int64_t)a.nseq * a.Hk * a.V >= INT32_MAX) return fail(SSD_ERR_UNSUPPORTED, "batch*nkvheads too large");
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.log_decay = log_decay;
+    a.scale = scale;
+    a.o = o;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (p.bf16) dispatch_la_update<__nv_bfloat16>(p, state, pages, a.nseq, st);
+    else dispatch_la_update<float>(p, state, pages, a.nseq, st);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "kernel launch (linear attention update)");
+    t_launches = 1;
+    t_last_error.clear();
+    return SSD_OK;
+}
+
+// ---------------------------------------------------------------------------------
+// Pages of a state cache.
+namespace ssd {
+namespace {
+
+struct PagesWork {
+    pages::Meta m;
+    pages::Moves mv;
+    int32_t* fresh = nullptr;
+    char* ws = nullptr;
+    bool owned = false;
+};
+
+size_t pages_bytes(const ssd_page_pool* p, int64_t n) {
+    // count, then src, dst and the new pages; compaction moves at most n_pages / 2 pages
+    const int64_t most = std::max<int64_t>(n, p->n_pages);
+    return align_up(64 + 3 * align_up(sizeof(int32_t) * (size_t)most, 64), 256);
+}
+
+ssd_status pages_check(const ssd_page_pool* p, int32_t n) {
+    if (!p) return fail(SSD_ERR_INVALID_ARG, "pool is NULL");
+    if (n < 0) return fail(SSD_ERR_INVALID_ARG, "n must be >= 0");
+    if (p->n_pages < 1 || p->n_rows < 1 || p->max_pages < 1)
+        return fail(SSD_ERR_INVALID_ARG, "n_pages, n_rows and max_pages must be positive");
+    if (p->n_pages > pages::kMaxIndex || p->n_rows > pages::kMaxIndex)
+        return fail(SSD_ERR_UNSUPPORTED, "more than 2^20 pages or rows");
+    if (p->n_arrays < 0) return fail(SSD_ERR_INVALID_ARG, "n_arrays must be >= 0");
+    if (p->n_arrays > pages::kMaxArrays) return fail(SSD_ERR_UNSUPPORTED, "more than %d arrays", pages::kMaxArrays);
+    if (p->n_arrays > 0 && (!p->arrays || !p->page_bytes))
+        return fail(SSD_ERR_INVALID_ARG, "arrays and page_bytes must be non-NULL");
+    for (int i = 0; i < p->n_arrays; ++i)
+        if (!p->arrays[i] || p->page_bytes[i] <= 0)
+            return fail(SSD_ERR_INVALID_ARG, "array %d is NULL or has no bytes", i);
+    if (!p->refcount || !p->table || !p->length || !p->live)
+        return fail(SSD_ERR_INVALID_ARG, "refcount, table, length and live must be non-NULL");
+    if (!aligned(p->refcount, 4) || !aligned(p->table, 4) || !aligned(p->length, 4) || !aligned(p->live, 4))
+        return fail(SSD_ERR_INVALID_ARG, "the pool's metadata must be 4-byte aligned");
+    return SSD_OK;
+}
+
+// The tiles of a page over all arrays; false where their number does not fit.
+bool pages_arrays(const ssd_page_pool* p, pages::Arrays* ar) {
+    int64_t tiles = 0;
+    ar->n = p->n_arrays;
+    for (int i = 0; i < p->n_arrays; ++i) {
+        ar->base[i] = static_cast<char*>(p->arrays[i]);
+        ar->bytes[i] = p->page_bytes[i];
+        ar->first[i] = (int32_t)tiles;
+        tiles += (p->page_bytes[i] + pages::kTile - 1) / pages::kTile;
+        if (tiles > INT32_MAX) return false;
+    }
+    ar->first[p->n_arrays] = (int32_t)tiles;
+    return true;
+}
+
+ssd_status pages_begin(const ssd_page_pool* p, int32_t n, cudaStream_t st, PagesWork* w) {
+    w->m = {p->refcount, p->table, p->length, p->live, p->n_pages, p->n_rows, p->max_pages};
+    const size_t bytes = pages_bytes(p, n);
+    w->ws = static_cast<char*>(p->workspace);
+    if (w->ws) {
+        if (p->workspace_bytes < bytes)
+            return fail(SSD_ERR_INVALID_ARG, "workspace_bytes %zu < required %zu", p->workspace_bytes, bytes);
+        if (!aligned(w->ws, 256)) return fail(SSD_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    } else {
+        const cudaError_t e = cudaMallocAsync(reinterpret_cast<void**>(&w->ws), bytes, st);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaMallocAsync(workspace)");
+        w->owned = true;
+    }
+    const size_t part = align_up(sizeof(int32_t) * (size_t)std::max<int64_t>(n, p->n_pages), 64);
+    w->mv.count = reinterpret_cast<int32_t*>(w->ws);
+    w->mv.src = reinterpret_cast<int32_t*>(w->ws + 64);
+    w->mv.dst = reinterpret_cast<int32_t*>(w->ws + 64 + part);
+    w->fresh = reinterpret_cast<int32_t*>(w->ws + 64 + 2 * part);
+    return SSD_OK;
+}
+
+ssd_status pages_end(PagesWork* w, ssd_status s, int launches, cudaStream_t st) {
+    cudaError_t e = cudaGetLastError();
+    if (w->owned) {
+        const cudaError_t f = cudaFreeAsync(w->ws, st);
+        if (e == cudaSuccess) e = f;
+    }
+    if (s != SSD_OK) return s;
+    if (e != cudaSuccess) return cuda_fail(e, "kernel launch (pages)");
+    t_launches = launches;
+    t_last_error.clear();
+    return SSD_OK;
+}
+
+template <pages::Op OP>
+ssd_status pages_plan(const PagesWork& w, const int32_t* a, const int32_t* b, int32_t n, int copy_last, cudaStream_t st) {
+    const size_t bits = align_up(((size_t)(OP == pages::COPY ? w.m.n_pages : w.m.n_rows) + 31) / 32 * 4, 16);
+    if (bits > 40 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(pages::k_pages_plan<OP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)bits);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(pages)");
+    }
+    StageScope sc(ST_PAGES_PLAN, st);
+    pages::k_pages_plan<OP><<<1, pages::kThreads, bits, st>>>(w.m, a, b, n, copy_last, w.fresh, w.mv);
+    return SSD_OK;
+}
+
+void pages_move(const PagesWork& w, const pages::Arrays& ar, int64_t most_moves, const int32_t* remap, cudaStream_t st) {
+    int64_t items = most_moves * ar.first[ar.n];
+    if (remap) items = std::max(items, ((int64_t)w.m.n_rows * (w.m.max_pages + 1) + pages::kMoveThreads - 1) / pages::kMoveThreads);
+    const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(items, (int64_t)sm_count() * 4));
+    StageScope sc(ST_PAGES_MOVE, st);
+    pages::k_pages_move<<<(unsigned)grid, pages::kMoveThreads, 0, st>>>(ar, w.mv, w.m, remap);
+}
+
+template <pages::Op OP>
+ssd_status pages_call(const ssd_page_pool* pool, const int32_t* a, const int32_t* b, int32_t n, int copy_last,
+                      bool moves, ssd_stream_t stream) {
+    ssd_status s = pages_check(pool, n);
+    if (s != SSD_OK) return s;
+    if (n > 0 && (!a || ((OP == pages::FORK || OP == pages::COPY) && !b)))
+        return fail(SSD_ERR_INVALID_ARG, "the request's lists must be non-NULL");
+    if (!aligned(a, 4) || !aligned(b, 4)) return fail(SSD_ERR_INVALID_ARG, "the request's lists must be 4-byte aligned");
+    pages::Arrays ar;
+    if (!pages_arrays(pool, &ar)) return fail(SSD_ERR_UNSUPPORTED, "a page has too many bytes");
+    if (n == 0) {
+        t_launches = 0;
+        t_last_error.clear();
+        return SSD_OK;
+    }
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    PagesWork w;
+    s = pages_begin(pool, n, st, &w);
+    if (s != SSD_OK) return s;
+    s = pages_plan<OP>(w, a, b, n, copy_last, st);
+    if (s == SSD_OK && moves) pages_move(w, ar, n, nullptr, st);
+    return pages_end(&w, s, moves ? 2 : 1, st);
+}
+
+}  // namespace
+}  // namespace ssd
+
+extern "C" ssd_status ssd_pages_workspace_size(const ssd_page_pool* pool, int32_t n, size_t* bytes) {
+    if (!bytes) return fail(SSD_ERR_INVALID_ARG, "bytes is NULL");
+    const ssd_status s = pages_check(pool, n);
+    if (s != SSD_OK) return s;
+    *bytes = pages_bytes(pool, n);
+    t_last_error.clear();
+    return SSD_OK;
+}
+
+extern "C" ssd_status ssd_pages_append(const ssd_page_pool* pool, const int32_t* rows, int32_t n, int copy_last,
+                                       ssd_stream_t stream) {
+    return pages_call<pages::APPEND>(pool, rows, nullptr, n, copy_last, copy_last != 0, stream);
+}
+
+extern "C" ssd_status ssd_pages_fork(const ssd_page_pool* pool, const int32_t* parents, const int32_t* children, int32_t n,
+                                     ssd_stream_t stream) {
+    return pages_call<pages::FORK>(pool, parents, children, n, 1, true, stream);
+}
+
+extern "C" ssd_status ssd_pages_free(const ssd_page_pool* pool, const int32_t* rows, int32_t n, ssd_stream_t stream) {
+    return pages_call<pages::FREE>(pool, rows, nullptr, n, 0, false, stream);
+}
+
+extern "C" ssd_status ssd_pages_copy(const ssd_page_pool* pool, const int32_t* src, const int32_t* dst, int32_t n,
+                                     ssd_stream_t stream) {
+    return pages_call<pages::COPY>(pool, src, dst, n, 1, true, stream);
+}
+
+extern "C" ssd_status ssd_pages_compact(const ssd_page_pool* pool, int32_t* remap, int32_t* counts, ssd_stream_t stream) {
+    ssd_status s = pages_check(pool, 0);
+    if (s != SSD_OK) return s;
+    if (!remap || !counts) return fail(SSD_ERR_INVALID_ARG, "remap and counts must be non-NULL");
+    if (!aligned(remap, 4) || !aligned(counts, 4)) return fail(SSD_ERR_INVALID_ARG, "remap and counts must be 4-byte aligned");
+    pages::Arrays ar;
+    if (!pages_arrays(pool, &ar)) return fail(SSD_ERR_UNSUPPORTED, "a page has too many bytes");
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    PagesWork w;
+    s = pages_begin(pool, 0, st, &w);
+    if (s != SSD_OK) return s;
+    {
+        StageScope sc(ST_PAGES_PLAN, st);
+        pages::k_pages_compact<<<1, pages::kThreads, 0, st>>>(w.m, remap, counts, w.mv);
+    }
+    pages_move(w, ar, pool->n_pages / 2, remap, st);
+    return pages_end(&w, SSD_OK, 2, st);
 }

@@ -1,0 +1,424 @@
+// Linear attention with a decay for each key/value head: what the prompt and the
+// single-token kernels share, the CUDA-core prompt kernel, and the single-token kernel.
+//
+// For every sequence and key/value head g (query heads h = g*R .. g*R+R-1 share it, R =
+// H/Hk), lam = exp(log_decay[g]) <= 1:
+//
+//     S_t = lam S_{t-1} + v_t k_t^T          FP32, stored [V][K] with K contiguous
+//     o_t[h] = scale * S_t q_t[h]
+//
+// Prompts are evaluated in chunks of C tokens. With S the state entering a chunk of len
+// tokens, t and s counted from its first token:
+//
+//     o_t = scale * ( sum_{s<=t} lam^(t-s) (q_t.k_s) v_s + lam^(t+1) S q_t )
+//     S' = lam^len S + sum_s lam^(len-1-s) v_s k_s^T
+//
+// All exponents are >= 0, so nothing overflows. Powers of lam that multiply the state
+// again and again (lam, lam^len) are kept as a sum of two floats: with one float the
+// relative error of lam^C (2^-25) would grow with the number of chunks the state
+// remembers (1 / (1 - lam^C), thousands for slow decays).
+#pragma once
+
+#include "ssd_common.cuh"
+
+namespace ssd {
+namespace la {
+
+// ---------------------------------------------------------------------------------
+// One prompt call as the kernels see it.
+struct Args {
+    const void* q;
+    const void* k;
+    const void* v;
+    const float* log_decay;
+    const float* init;           // [nseq or pages, Hk, V, K] or null
+    const int32_t* init_pages;   // [nseq] or null
+    float* fin;                  // [nseq or pages, Hk, V, K] or null
+    const int32_t* fin_pages;    // [nseq] or null
+    void* o;
+    float* slots;                // segment states [slot][Hk][V][K]
+    const ChunkEntry* table;     // packed: segment table, else null
+    const int32_t* first;
+    const int32_t* count;
+    const int32_t* order;
+    int64_t q_stride, k_stride, v_stride;   // elements between tokens
+    int64_t seqlen, npages;
+    float scale;
+    int32_t nseq, nps;           // dense: segments per sequence
+    int32_t Ls;                  // tokens per segment
+    int32_t H, Hk, R, K, V;
+    int32_t stall;               // test hook: the tensor-core kernel's UMMA warp waits for nothing
+};
+
+// One segment: tokens [start, start + len) of the packed rows, number j of the n segments
+// of sequence seq, whose state slots begin at slot0. Slot slot0 holds a copy of the
+// sequence's initial state (the state may be replaced in place while other segments'
+// CTAs still run), slot0 + i the state that segment i-1 alone adds.
+struct Seg {
+    int32_t seq, j, n, slot0, len;
+    int64_t start;
+};
+
+// Segment `i` of a pass; false where a packed call has fewer. A state pass (OUT false)
+// has no CTAs for a dense sequence's last segment, and its packed CTAs of one return.
+template <bool OUT>
+__device__ __forceinline__ bool find_seg(const Args& a, int i, Seg* s) {
+    if (a.table) {
+        if (i >= *a.count) return false;
+        const ChunkEntry e = a.table[a.order[i]];
+        s->seq = e.seq;
+        s->start = e.start;
+        s->len = e.len;
+        s->slot0 = a.first[e.seq];
+        s->n = a.first[e.seq + 1] - s->slot0;
+        s->j = e.pad - s->slot0;
+        return OUT || s->j + 1 < s->n;
+    }
+    const int per = OUT ? a.nps : a.nps - 1;
+    s->seq = i / per;
+    s->j = i % per;
+    s->n = a.nps;
+    s->slot0 = s->seq * a.nps;
+    s->start = (int64_t)s->seq * a.seqlen + (int64_t)s->j * a.Ls;
+    s->len = (int32_t)min((int64_t)a.Ls, a.seqlen - (int64_t)s->j * a.Ls);
+    return true;
+}
+
+// Where sequence s's state is in an array of states: its page, or s without a page list.
+// -1 stands for "none"; a page outside the pool is an error and stands for none too.
+__device__ __forceinline__ int64_t page_of(const int32_t* pages, int64_t npages, int32_t s) {
+    if (!pages) return s;
+    const int32_t p = pages[s];
+    if (p < -1 || p >= npages) {
+        latch_error(SSD_ERR_INVALID_ARG);
+        return -1;
+    }
+    return p;
+}
+
+// Whether sequence s must not write its final state to page p: an earlier sequence writes
+// the same page, or another one starts from it in this call. Called by the whole block.
+__device__ __forceinline__ bool page_clash(const Args& a, int32_t s, int64_t p, int threads) {
+    int bad = 0;
+    const bool one_pool = a.init == a.fin;
+    for (int32_t i = threadIdx.x; i < a.nseq; i += threads) {
+        if (i == s) continue;
+        if (i < s && a.fin_pages && a.fin_pages[i] == p) bad = 1;
+        if (one_pool && (a.init_pages ? a.init_pages[i] : i) == p) bad = 1;
+    }
+    return __syncthreads_or(bad) != 0;
+}
+
+// lam^n as hi + lo; hi is lam^n rounded to float.
+__device__ __forceinline__ float2 pow2f(double g, int64_t n) {
+    const double e = exp(g * (double)n);
+    const float hi = (float)e;
+    return make_float2(hi, (float)(e - (double)hi));
+}
+
+__device__ __forceinline__ void check_decay(float g) {
+    if (!(g <= 0.f) || isinf(g)) latch_error(SSD_ERR_INVALID_ARG);
+}
+
+// ---------------------------------------------------------------------------------
+// CUDA-core prompt kernel (FP32 arithmetic throughout). One CTA per (segment, key/value
+// head, 64 columns of V); chunks of 64 tokens in shared memory; the state in shared
+// memory as [K][64]. Without OUT: only the state that the segment adds.
+constexpr int kSimtC = 64;           // tokens per chunk
+constexpr int kSimtV = 64;           // V columns per CTA
+constexpr int kSimtThreads = 256;
+
+__host__ __device__ constexpr int simt_ld(int K) { return K + 4; }   // row stride: no bank conflict of 8 rows
+__host__ __device__ constexpr size_t simt_smem(int K, bool out) {
+    return sizeof(float) * ((size_t)(out ? 2 : 1) * kSimtC * simt_ld(K) + kSimtC * kSimtV + (size_t)K * kSimtV +
+                            (out ? kSimtC * (kSimtC + 4) : 0) + kSimtC + 4);
+}
+
+template <typename T, bool OUT>
+__global__ void __launch_bounds__(kSimtThreads) k_la_simt(const __grid_constant__ Args a) {
+    constexpr int C = kSimtC, VB = kSimtV, NT = kSimtThreads;
+    const int nvb = (a.V + VB - 1) / VB;
+    const int vb = blockIdx.x % nvb, g = (blockIdx.x / nvb) % a.Hk;
+    Seg sg;
+    if (!find_seg<OUT>(a, blockIdx.x / nvb / a.Hk, &sg)) return;
+    const int K = a.K, V = a.V, ldk = simt_ld(K), tid = threadIdx.x;
+    const int v0 = vb * VB, nv = min(VB, V - v0);
+
+    extern __shared__ __align__(16) float smem[];
+    float* sk = smem;                        // [C][ldk]
+    float* sv = sk + C * ldk;                // [C][VB]
+    float* sS = sv + C * VB;                 // [K][VB]
+    float* pw = sS + K * VB;                 // lam^0 .. lam^C
+    float* sq = pw + C + 4;                  // [C][ldk]
+    float* sP = sq + C * ldk;                // [C][C + 4]
+    __shared__ float2 lam_seg;
+
+    const float gd = a.log_decay[g];
+    if (tid <= C) pw[tid] = (float)exp((double)gd * tid);
+    if (tid == 0) {
+        check_decay(gd);
+        lam_seg = pow2f(gd, a.Ls);
+    }
+    const int64_t per_state = (int64_t)a.Hk * V * K, head = ((int64_t)g * V + v0) * K;
+    const int64_t ip = a.init ? page_of(a.init_pages, a.npages, sg.seq) : -1;
+    const bool last = sg.j + 1 == sg.n;
+    int64_t fp = -1;
+    if (OUT && last && a.fin) {
+        fp = page_of(a.fin_pages, a.npages, sg.seq);
+        if (a.fin_pages && fp >= 0 && page_clash(a, sg.seq, fp, NT)) {
+            latch_error(SSD_ERR_INVALID_ARG);
+            fp = -1;
+        }
+    }
+    __syncthreads();
+    // State entering the segment (zero-start without OUT); [V][K] in memory, [K][VB] here.
+    for (int e = tid; e < K * VB; e += NT) {
+        const int kk = e % K, vv = e / K;
+        const int64_t at = head + (int64_t)vv * K + kk;
+        float s = 0.f;
+        if (vv < nv) {
+            if (OUT) {
+                if (ip >= 0) s = sg.n == 1 ? a.init[ip * per_state + at] : a.slots[(int64_t)sg.slot0 * per_state + at];
+                for (int i = 1; i <= sg.j; ++i)
+                    s = fmaf(lam_seg.x, s, fmaf(lam_seg.y, s, a.slots[(int64_t)(sg.slot0 + i) * per_state + at]));
+            } else if (sg.j == 0 && ip >= 0) {
+                a.slots[(int64_t)sg.slot0 * per_state + at] = a.init[ip * per_state + at];
+            }
+        }
+        sS[kk * VB + vv] = s;
+    }
+
+    const T* kp = static_cast<const T*>(a.k) + sg.start * a.k_stride + (int64_t)g * K;
+    const T* vp = static_cast<const T*>(a.v) + sg.start * a.v_stride + (int64_t)g * V + v0;
+    const bool need_last = !OUT || fp >= 0;
+    for (int c0 = 0; c0 < sg.len; c0 += C) {
+        const int len = min(C, sg.len - c0);
+        __syncthreads();                     // the last chunk's readers of sk, sv are done
+        for (int e = tid; e < C * (K / 4); e += NT) {
+            const int t = e / (K / 4), c4 = e % (K / 4);
+            const float4 x = t < len ? load4(kp + (int64_t)(c0 + t) * a.k_stride + 4 * c4) : make_float4(0, 0, 0, 0);
+            *reinterpret_cast<float4*>(sk + t * ldk + 4 * c4) = x;
+        }
+        for (int e = tid; e < C * (VB / 4); e += NT) {
+            const int t = e / (VB / 4), c4 = e % (VB / 4);
+            const float4 x = t < len && 4 * c4 < nv ? load4(vp + (int64_t)(c0 + t) * a.v_stride + 4 * c4)
+                                                    : make_float4(0, 0, 0, 0);
+            *reinterpret_cast<float4*>(sv + t * VB + 4 * c4) = x;
+        }
+        if (OUT) {
+            for (int r = 0; r < a.R; ++r) {
+                const T* qp = static_cast<const T*>(a.q) + (sg.start + c0) * a.q_stride + (int64_t)(g * a.R + r) * K;
+                __syncthreads();             // readers of sq, sP are done
+                for (int e = tid; e < C * (K / 4); e += NT) {
+                    const int t = e / (K / 4), c4 = e % (K / 4);
+                    const float4 x = t < len ? load4(qp + (int64_t)t * a.q_stride + 4 * c4) : make_float4(0, 0, 0, 0);
+                    *reinterpret_cast<float4*>(sq + t * ldk + 4 * c4) = x;
+                }
+                __syncthreads();
+                const int tx = tid & 15, ty = tid >> 4;   // rows ty + 16 i, columns tx + 16 j / 4 tx + j
+                {
+                    float acc[4][4] = {};
+                    for (int kk = 0; kk < K; kk += 4) {
+                        float4 x[4], y[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            x[i] = *reinterpret_cast<const float4*>(sq + (ty + 16 * i) * ldk + kk);
+                            y[i] = *reinterpret_cast<const float4*>(sk + (tx + 16 * i) * ldk + kk);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                acc[i][j] = fmaf(x[i].x, y[j].x, acc[i][j]);
+                                acc[i][j] = fmaf(x[i].y, y[j].y, acc[i][j]);
+                                acc[i][j] = fmaf(x[i].z, y[j].z, acc[i][j]);
+                                acc[i][j] = fmaf(x[i].w, y[j].w, acc[i][j]);
+                            }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int t = ty + 16 * i, s = tx + 16 * j;
+                            sP[t * (C + 4) + s] = s <= t ? acc[i][j] * pw[t - s] : 0.f;
+                        }
+                }
+                __syncthreads();
+                float acc[4][4] = {}, inter[4][4] = {};
+                for (int s = 0; s < ty + 49; ++s) {       // sources up to this thread's last row
+                    const float4 y = *reinterpret_cast<const float4*>(sv + s * VB + 4 * tx);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float x = sP[(ty + 16 * i) * (C + 4) + s];
+                        if (s > ty + 16 * i) continue;
+                        acc[i][0] = fmaf(x, y.x, acc[i][0]);
+                        acc[i][1] = fmaf(x, y.y, acc[i][1]);
+                        acc[i][2] = fmaf(x, y.z, acc[i][2]);
+                        acc[i][3] = fmaf(x, y.w, acc[i][3]);
+                    }
+                }
+                for (int kk = 0; kk < K; ++kk) {
+                    const float4 y = *reinterpret_cast<const float4*>(sS + kk * VB + 4 * tx);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float x = sq[(ty + 16 * i) * ldk + kk];
+                        inter[i][0] = fmaf(x, y.x, inter[i][0]);
+                        inter[i][1] = fmaf(x, y.y, inter[i][1]);
+                        inter[i][2] = fmaf(x, y.z, inter[i][2]);
+                        inter[i][3] = fmaf(x, y.w, inter[i][3]);
+                    }
+                }
+                T* op = static_cast<T*>(a.o) + ((sg.start + c0) * a.H + g * a.R + r) * (int64_t)V + v0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int t = ty + 16 * i;
+                    if (t >= len || 4 * tx >= nv) continue;
+                    const float w = pw[t + 1];
+                    T* p = op + (int64_t)t * a.H * V + 4 * tx;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) p[j] = from_f32<T>(a.scale * fmaf(w, inter[i][j], acc[i][j]));
+                }
+            }
+        }
+        __syncthreads();
+        if (c0 + C < sg.len || need_last) {
+            // S = lam^len S + sum_s lam^(len-1-s) k_s v_s^T; rows kk = ty + 16 i, columns 4 tx
+            const float2 lc = pow2f(gd, len);
+            const int tx = tid & 15, ty = tid >> 4;
+            for (int kb = ty; kb < K; kb += 64) {
+                float acc[4][4] = {};
+                for (int s = 0; s < len; ++s) {
+                    const float w = pw[len - 1 - s];
+                    const float4 y = *reinterpret_cast<const float4*>(sv + s * VB + 4 * tx);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float x = kb + 16 * i < K ? w * sk[s * ldk + kb + 16 * i] : 0.f;
+                        acc[i][0] = fmaf(x, y.x, acc[i][0]);
+                        acc[i][1] = fmaf(x, y.y, acc[i][1]);
+                        acc[i][2] = fmaf(x, y.z, acc[i][2]);
+                        acc[i][3] = fmaf(x, y.w, acc[i][3]);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (kb + 16 * i >= K) continue;
+                    float* s = sS + (kb + 16 * i) * VB + 4 * tx;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[j] = fmaf(lc.x, s[j], fmaf(lc.y, s[j], acc[i][j]));
+                }
+            }
+        }
+    }
+    __syncthreads();
+    float* dst = OUT ? (fp >= 0 ? a.fin + fp * per_state : nullptr) : a.slots + (int64_t)(sg.slot0 + sg.j + 1) * per_state;
+    if (dst)
+        for (int e = tid; e < K * nv; e += NT) dst[head + e] = sS[(e % K) * VB + e / K];
+}
+
+// ---------------------------------------------------------------------------------
+// Single tokens: S <- lam S + v k^T in place and o = scale * S q for one token of every
+// batch row. The FP32 state (64 KiB per head at 128 x 128) is read and written once and
+// is all the traffic that counts, so the kernel is an HBM stream: a state row of K floats
+// is LPR lanes of 16 bytes, a warp keeps 8 rows per lane group in flight before it writes
+// any, and one state serves all R query heads that share it.
+constexpr int kTokThreads = 128;
+constexpr int kTokRows = 8;          // state rows in flight per lane group
+
+template <typename T, int LPR>
+__global__ void __launch_bounds__(kTokThreads)
+k_la_update(float* __restrict__ state, const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
+            const float* __restrict__ log_decay, float scale, const int32_t* __restrict__ pages, int64_t npages,
+            T* __restrict__ o, int nvs, int Hk, int R, int K, int V, int64_t qs, int64_t ks, int64_t vs) {
+    constexpr int GPW = 32 / LPR;                        // lane groups (rows of one load) per warp
+    constexpr int U = kTokRows, WARPS = kTokThreads / 32;
+    constexpr int RPB = U * GPW * WARPS;                 // state rows per CTA
+    const int vsp = blockIdx.x % nvs, g = (blockIdx.x / nvs) % Hk;
+    const int64_t b = blockIdx.x / nvs / Hk;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c4 = lane % LPR, grp = lane / LPR;
+    int64_t page = b;
+    if (pages) {
+        page = pages[b];
+        if (page < 0 || page >= npages) {                // -1: a padded row, left as it is
+            if (page != -1 && threadIdx.x == 0) latch_error(SSD_ERR_INVALID_ARG);
+            return;
+        }
+    }
+    float* st = state + (page * Hk + g) * (int64_t)V * K;
+    // this lane group's rows: r0 + u * GPW, columns 4 c4 ..
+    const int r0 = vsp * RPB + warp * U * GPW + grp;
+    const bool col = 4 * c4 < K;
+    float4 s[U];
+    float vr[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int row = r0 + u * GPW;
+        const bool ok = col && row < V;
+        s[u] = ok ? __ldcs(reinterpret_cast<const float4*>(st + (int64_t)row * K + 4 * c4)) : make_float4(0, 0, 0, 0);
+        vr[u] = row < V ? to_f32(v[b * vs + (int64_t)g * V + row]) : 0.f;
+    }
+    const float4 kv = col ? load4(k + b * ks + (int64_t)g * K + 4 * c4) : make_float4(0, 0, 0, 0);
+    if (pages) {
+        // A page named twice would be updated by two blocks at once: the first row keeps
+        // it, the others are refused.
+        int dup = 0;
+        for (int64_t i = threadIdx.x; i < b; i += kTokThreads) dup |= pages[i] == page;
+        if (__syncthreads_or(dup)) {
+            if (threadIdx.x == 0) latch_error(SSD_ERR_INVALID_ARG);
+            return;
+        }
+    }
+    const float gd = log_decay[g];
+    if (threadIdx.x == 0) check_decay(gd);
+    // lam = hi + lo: 1 + expm1(g) with the rounding of the sum kept
+    const float m1 = expm1f(gd), hi = 1.f + m1, lo = m1 - (hi - 1.f);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int row = r0 + u * GPW;
+        s[u].x = fmaf(hi, s[u].x, fmaf(lo, s[u].x, vr[u] * kv.x));
+        s[u].y = fmaf(hi, s[u].y, fmaf(lo, s[u].y, vr[u] * kv.y));
+        s[u].z = fmaf(hi, s[u].z, fmaf(lo, s[u].z, vr[u] * kv.z));
+        s[u].w = fmaf(hi, s[u].w, fmaf(lo, s[u].w, vr[u] * kv.w));
+        if (col && row < V) __stcs(reinterpret_cast<float4*>(st + (int64_t)row * K + 4 * c4), s[u]);
+    }
+    const T* qb = q + b * qs + (int64_t)g * R * K;
+    T* ob = o + ((b * Hk + g) * (int64_t)R) * V;
+    for (int r = 0; r < R; ++r) {
+        const float4 qv = col ? load4(qb + (int64_t)r * K + 4 * c4) : make_float4(0, 0, 0, 0);
+        float d[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) d[u] = fmaf(s[u].x, qv.x, fmaf(s[u].y, qv.y, fmaf(s[u].z, qv.z, s[u].w * qv.w)));
+        // Sum over the LPR lanes of a group. While more than one row is left per lane, a
+        // lane gives half of its rows to its partner (U, U/2, .. shuffles in all instead
+        // of U per step); then plain butterflies.
+        int n = U, off = LPR / 2, mine = 0;
+#pragma unroll
+        for (int st2 = 0; st2 < 3; ++st2) {
+            if (off >= 1 && n > 1) {
+                const bool up = (c4 & off) != 0;
+#pragma unroll
+                for (int i = 0; i < U / 2; ++i)
+                    if (i < n / 2) {
+                        const float give = up ? d[i] : d[i + n / 2], keep = up ? d[i + n / 2] : d[i];
+                        d[i] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+                    }
+                n /= 2;
+                mine += up ? n : 0;
+                off /= 2;
+            }
+        }
+#pragma unroll
+        for (int w = LPR / 16; w >= 1; w /= 2) d[0] += __shfl_xor_sync(0xffffffffu, d[0], w);
+        // each lane group's lanes with the low bits clear hold rows mine .. mine + n - 1
+        if (LPR <= 8 || (c4 & (LPR / 8 - 1)) == 0) {
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                if (i < n) {
+                    const int row = r0 + (mine + i) * GPW;
+                    if (row < V) ob[(int64_t)r * V + row] = from_f32<T>(scale * d[i]);
+                }
+        }
+    }
+}
+
+}  // namespace la
+}  // namespace ssd

@@ -11,6 +11,8 @@ Functions mirror the C entry points:
            chunk=128, y=None, final_state=None, workspace=None)
   state_update(state, x, dt_raw, dt_bias, A, B, C, D, y=None)
   ChunkCache.empty(...), strict_scan_fwd(...), strict_state_update(...)  (strict mode)
+  linear_attn_fwd(q, k, v, log_decay, ...), linear_attn_update(state, q, k, v, log_decay, ...)
+  PagePool(...), pages_append/fork/free/compact/copy(pool, ...)  (pages of a state cache)
   device_status(), scan_variant(...), workspace_size(...), last_launch_count()
 """
 from __future__ import annotations
@@ -30,9 +32,10 @@ if not os.path.exists(LIB_PATH):
 
 _lib = ctypes.CDLL(LIB_PATH)
 
-SSD_OK, SSD_ERR_INVALID_ARG, SSD_ERR_UNSUPPORTED, SSD_ERR_CUDA, SSD_ERR_TIMEOUT = range(5)
+SSD_OK, SSD_ERR_INVALID_ARG, SSD_ERR_UNSUPPORTED, SSD_ERR_CUDA, SSD_ERR_TIMEOUT, SSD_ERR_NO_PAGES = range(6)
 SSD_DTYPE_F32, SSD_DTYPE_BF16 = 0, 1
-_STATUS = {1: "SSD_ERR_INVALID_ARG", 2: "SSD_ERR_UNSUPPORTED", 3: "SSD_ERR_CUDA", 4: "SSD_ERR_TIMEOUT"}
+_STATUS = {1: "SSD_ERR_INVALID_ARG", 2: "SSD_ERR_UNSUPPORTED", 3: "SSD_ERR_CUDA", 4: "SSD_ERR_TIMEOUT",
+           5: "SSD_ERR_NO_PAGES"}
 
 
 class SSDDims(ctypes.Structure):
@@ -111,6 +114,45 @@ _lib.ssd_strict_state_update.argtypes = [ctypes.POINTER(SSDChunkCache), _p, _p, 
 _lib.ssd_strict_state_update.restype = ctypes.c_int
 _lib.ssd_last_launch_count.argtypes = []
 _lib.ssd_last_launch_count.restype = ctypes.c_int
+
+
+class SSDLinearAttnDims(ctypes.Structure):
+    """Mirror of ``ssd_linear_attn_dims``."""
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("nseq", ctypes.c_int32),
+                ("total_tokens", ctypes.c_int64), ("nheads", ctypes.c_int32), ("nkvheads", ctypes.c_int32),
+                ("headdim_k", ctypes.c_int32), ("headdim_v", ctypes.c_int32), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64), ("n_pages", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class SSDPagePool(ctypes.Structure):
+    """Mirror of ``ssd_page_pool``."""
+    _fields_ = [("n_pages", ctypes.c_int32), ("n_rows", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("n_arrays", ctypes.c_int32), ("arrays", ctypes.POINTER(ctypes.c_void_p)),
+                ("page_bytes", ctypes.POINTER(ctypes.c_int64)), ("refcount", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("length", ctypes.c_void_p), ("live", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+_lib.ssd_linear_attn_fwd_workspace_size.argtypes = [ctypes.POINTER(SSDLinearAttnDims), ctypes.POINTER(ctypes.c_size_t)]
+_lib.ssd_linear_attn_fwd_workspace_size.restype = ctypes.c_int
+_lib.ssd_linear_attn_fwd.argtypes = [_p, _p, _p, _p, ctypes.c_float, _p, _p, _p, _p, _p, _p,
+                                     ctypes.POINTER(SSDLinearAttnDims), _p]
+_lib.ssd_linear_attn_fwd.restype = ctypes.c_int
+_lib.ssd_linear_attn_update.argtypes = [_p, _p, _p, _p, _p, ctypes.c_float, _p, _p, ctypes.POINTER(SSDLinearAttnDims), _p]
+_lib.ssd_linear_attn_update.restype = ctypes.c_int
+_lib.ssd_pages_workspace_size.argtypes = [ctypes.POINTER(SSDPagePool), ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)]
+_lib.ssd_pages_workspace_size.restype = ctypes.c_int
+_lib.ssd_pages_append.argtypes = [ctypes.POINTER(SSDPagePool), _p, ctypes.c_int32, ctypes.c_int, _p]
+_lib.ssd_pages_append.restype = ctypes.c_int
+_lib.ssd_pages_fork.argtypes = [ctypes.POINTER(SSDPagePool), _p, _p, ctypes.c_int32, _p]
+_lib.ssd_pages_fork.restype = ctypes.c_int
+_lib.ssd_pages_free.argtypes = [ctypes.POINTER(SSDPagePool), _p, ctypes.c_int32, _p]
+_lib.ssd_pages_free.restype = ctypes.c_int
+_lib.ssd_pages_compact.argtypes = [ctypes.POINTER(SSDPagePool), _p, _p, _p]
+_lib.ssd_pages_compact.restype = ctypes.c_int
+_lib.ssd_pages_copy.argtypes = [ctypes.POINTER(SSDPagePool), _p, _p, ctypes.c_int32, _p]
+_lib.ssd_pages_copy.restype = ctypes.c_int
 
 
 class SSDKernelTime(ctypes.Structure):
@@ -622,3 +664,232 @@ def strict_state_update(cache: ChunkCache, x, dt_raw, dt_bias, A, B, C, D, y=Non
                                             _ptr(C), _ptr(D), _ptr(y), ctypes.byref(dims), cache.chunk,
                                             _stream(dev)))
     return y
+
+
+# ---------------------------------------------------------------------------------
+# Linear attention with a decay for each head.
+def _token_stride(t, name, lead, heads, dim, dtype, device):
+    """Elements between consecutive tokens of t [*lead, heads, dim], a contiguous tensor or a
+    slice of one whose heads are contiguous (lead: (batch, L) or (T,))."""
+    shape = (*lead, heads, dim)
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.is_contiguous():
+        return heads * dim
+    st = t.stride()
+    if st[-1] != 1 or (heads > 1 and st[-2] != dim):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    if len(lead) == 1:
+        return st[0] if lead[0] > 1 else heads * dim
+    b, L = lead
+    if b > 1 and L > 1 and st[0] != L * st[1]:
+        raise ValueError(f"{name}: the sequences of a dense batch must follow each other without a gap")
+    return st[1] if L > 1 else st[0] if b > 1 else heads * dim
+
+
+def _pages_arg(pages, name, n, device):
+    if pages is not None:
+        _need(pages, name, (n,), torch.int32, device)
+
+
+def linear_attn_dims(lead, H, Hk, K, V, dtype_code, nseq=None, strides=(0, 0, 0), n_pages=0, workspace=None):
+    """ssd_linear_attn_dims of a dense (lead = (batch, L)) or packed (lead = (T,), nseq) call."""
+    d = SSDLinearAttnDims()
+    if nseq is None:
+        d.batch, d.seqlen = lead
+    else:
+        d.nseq, d.total_tokens = nseq, lead[0]
+    d.nheads, d.nkvheads, d.headdim_k, d.headdim_v = H, Hk, K, V
+    d.q_stride, d.k_stride, d.v_stride = strides
+    d.n_pages, d.dtype = n_pages, dtype_code
+    if workspace is not None:
+        d.workspace, d.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return d
+
+
+def linear_attn_workspace_size(dims: SSDLinearAttnDims) -> int:
+    b = ctypes.c_size_t(0)
+    _check(_lib.ssd_linear_attn_fwd_workspace_size(ctypes.byref(dims), ctypes.byref(b)))
+    return int(b.value)
+
+
+def linear_attn_fwd(q, k, v, log_decay, scale=None, init_state=None, init_pages=None, cu_seqlens=None, o=None,
+                    final_state=None, final_pages=None, workspace=None):
+    """Linear attention with a decay for each key/value head, prompts (ssd_linear_attn_fwd).
+
+    Dense: q [batch, L, H, K], k [batch, L, Hk, K], v [batch, L, Hk, V]; packed varlen
+    (cu_seqlens int32 [nseq+1] on the device): q [T, H, K], k [T, Hk, K], v [T, Hk, V]. They
+    may be slices of one tensor (heads contiguous). log_decay [Hk] float32, <= 0; scale
+    defaults to K**-0.5. init_state: [nseq, Hk, V, K] float32, or a pool [n_pages, Hk, V, K]
+    with init_pages int32 [nseq] (-1: zero). final_state likewise with final_pages (-1: not
+    written); it may be init_state itself.
+    Returns (o [..., H, V], final_state)."""
+    dev, dt = q.device, q.dtype
+    H, K = q.shape[-2:]
+    Hk, V = v.shape[-2:]
+    varlen = cu_seqlens is not None
+    lead = q.shape[:-2]
+    if len(lead) != (1 if varlen else 2):
+        raise ValueError("q must be [batch, L, H, K], or [T, H, K] with cu_seqlens")
+    nseq = cu_seqlens.numel() - 1 if varlen else lead[0]
+    strides = (_token_stride(q, "q", lead, H, K, dt, dev), _token_stride(k, "k", lead, Hk, K, dt, dev),
+               _token_stride(v, "v", lead, Hk, V, dt, dev))
+    _need(log_decay, "log_decay", (Hk,), torch.float32, dev)
+    if varlen:
+        _need(cu_seqlens, "cu_seqlens", (nseq + 1,), torch.int32, dev)
+    n_pages = 0
+    if final_pages is not None and final_state is None:
+        raise ValueError("final_pages needs final_state, the pool to write to")
+    if final_state is None:
+        final_state = torch.empty(nseq, Hk, V, K, dtype=torch.float32, device=dev)
+    for name, states, pages in (("init", init_state, init_pages), ("final", final_state, final_pages)):
+        if pages is None:
+            if states is not None:
+                _need(states, f"{name}_state", (nseq, Hk, V, K), torch.float32, dev)
+            continue
+        if states is None:
+            raise ValueError(f"{name}_pages needs {name}_state, the pool")
+        _pages_arg(pages, f"{name}_pages", nseq, dev)
+        if n_pages and states.shape[0] != n_pages:
+            raise ValueError("the pools of init_state and final_state must have the same number of pages")
+        n_pages = states.shape[0]
+        _need(states, f"{name}_state", (n_pages, Hk, V, K), torch.float32, dev)
+    if o is None:
+        o = torch.empty(*lead, H, V, dtype=dt, device=dev)
+    else:
+        _need(o, "o", (*lead, H, V), dt, dev)
+    dims = linear_attn_dims(lead, H, Hk, K, V, _dtype_code(q), nseq if varlen else None, strides, n_pages, workspace)
+    with torch.cuda.device(dev):
+        _check(_lib.ssd_linear_attn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), K ** -0.5 if scale is None else scale,
+                                        _ptr(init_state), _ptr(init_pages), _ptr(cu_seqlens), _ptr(o),
+                                        _ptr(final_state), _ptr(final_pages), ctypes.byref(dims), _stream(dev)))
+    return o, final_state
+
+
+def linear_attn_update(state, q, k, v, log_decay, scale=None, pages=None, o=None):
+    """One token of linear attention for every batch row (ssd_linear_attn_update), states
+    updated in place: state [batch, Hk, V, K] float32, or a pool [n_pages, Hk, V, K] with
+    pages int32 [batch] (-1: a padded row, left as it is). q [batch, H, K], k [batch, Hk, K],
+    v [batch, Hk, V], which may be slices of one tensor. Returns o [batch, H, V]."""
+    dev, dt = q.device, q.dtype
+    b, H, K = q.shape
+    Hk, V = v.shape[-2:]
+    lead = (b,)
+    strides = (_token_stride(q, "q", lead, H, K, dt, dev), _token_stride(k, "k", lead, Hk, K, dt, dev),
+               _token_stride(v, "v", lead, Hk, V, dt, dev))
+    _need(log_decay, "log_decay", (Hk,), torch.float32, dev)
+    n_pages = b if pages is None else state.shape[0]
+    _need(state, "state", (n_pages, Hk, V, K), torch.float32, dev)
+    _pages_arg(pages, "pages", b, dev)
+    if o is None:
+        o = torch.empty(b, H, V, dtype=dt, device=dev)
+    else:
+        _need(o, "o", (b, H, V), dt, dev)
+    dims = linear_attn_dims((b, 1), H, Hk, K, V, _dtype_code(q), None, strides, n_pages)
+    with torch.cuda.device(dev):
+        _check(_lib.ssd_linear_attn_update(_ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
+                                           K ** -0.5 if scale is None else scale, _ptr(pages), _ptr(o),
+                                           ctypes.byref(dims), _stream(dev)))
+    return o
+
+
+# ---------------------------------------------------------------------------------
+# Pages of a state cache.
+class PagePool:
+    """A pool of cache pages (``ssd_page_pool``): `arrays` are contiguous tensors
+    [n_pages, ...] on one device, a page being one index of all of them; the metadata
+    refcount [n_pages], table [n_rows, max_pages], length [n_rows] and live [n_rows] are int32
+    views of `meta` (made here, empty, unless given), so one copy of `meta` saves or restores
+    them all. `live` holds each row's live page (-1: none), a page list for the linear
+    attention calls. Tensors are owned here; the library only reads and writes them. Calls on
+    one pool share its workspace and metadata and must not overlap on the device."""
+
+    def __init__(self, arrays, n_rows, max_pages, meta=None):
+        arrays = list(arrays)
+        if not arrays:
+            raise ValueError("a pool needs at least one array")
+        n, dev = arrays[0].shape[0], arrays[0].device
+        for i, t in enumerate(arrays):
+            if not t.is_cuda or t.device != dev or t.shape[0] != n or not t.is_contiguous() or t.numel() == 0:
+                raise ValueError(f"array {i} must be a contiguous CUDA tensor [n_pages={n}, ...] on {dev}")
+        if n_rows < 1 or max_pages < 1:
+            raise ValueError("n_rows and max_pages must be positive")
+        size = n + n_rows * (max_pages + 2)
+        if meta is None:
+            meta = torch.full((size,), -1, dtype=torch.int32, device=dev)
+            meta[:n] = 0
+            meta[n + n_rows * max_pages:size - n_rows] = 0
+        _need(meta, "meta", (size,), torch.int32, dev)
+        self.arrays, self.meta, self.n_pages, self.n_rows, self.max_pages = arrays, meta, n, n_rows, max_pages
+        self.device = dev
+        self.refcount, table, self.length, self.live = meta.split([n, n_rows * max_pages, n_rows, n_rows])
+        self.table = table.view(n_rows, max_pages)
+        k = len(arrays)
+        c = SSDPagePool(n, n_rows, max_pages, k, (ctypes.c_void_p * k)(*[t.data_ptr() for t in arrays]),
+                        (ctypes.c_int64 * k)(*[t[0].numel() * t.element_size() for t in arrays]),
+                        self.refcount.data_ptr(), self.table.data_ptr(), self.length.data_ptr(), self.live.data_ptr())
+        self._c, self._ref = c, ctypes.byref(c)
+        self._reserve(max(n, n_rows))
+
+    def _reserve(self, n):
+        """Workspace for requests of up to n entries."""
+        b = ctypes.c_size_t(0)
+        _check(_lib.ssd_pages_workspace_size(self._ref, n, ctypes.byref(b)))
+        self.workspace = torch.empty(b.value, dtype=torch.uint8, device=self.device)
+        self._c.workspace, self._c.workspace_bytes = self.workspace.data_ptr(), b.value
+        self._most = n
+
+    def _list(self, t, name, n=None):
+        _need(t, name, (t.numel() if n is None else n,), torch.int32, self.device)
+        if t.numel() > self._most:
+            raise ValueError(f"{name} has more entries than the pool has pages or rows")
+        return t.numel()
+
+
+def pages_append(pool: PagePool, rows, copy_last=False):
+    """One more (live) page for each listed row, the lowest free ones (ssd_pages_append);
+    copy_last: it continues from a copy of the row's last page."""
+    n = pool._list(rows, "rows")
+    with torch.cuda.device(pool.device):
+        _check(_lib.ssd_pages_append(pool._ref, rows.data_ptr(), n, 1 if copy_last else 0, _stream(pool.device)))
+
+
+def pages_fork(pool: PagePool, parents, children):
+    """children[i] (empty rows) continue parents[i]: shared snapshots, a copied live page
+    (ssd_pages_fork)."""
+    n = pool._list(parents, "parents")
+    pool._list(children, "children", n)
+    with torch.cuda.device(pool.device):
+        _check(_lib.ssd_pages_fork(pool._ref, parents.data_ptr(), children.data_ptr(), n, _stream(pool.device)))
+
+
+def pages_free(pool: PagePool, rows):
+    """Empties the listed rows; pages that no row holds any more are free (ssd_pages_free)."""
+    n = pool._list(rows, "rows")
+    with torch.cuda.device(pool.device):
+        _check(_lib.ssd_pages_free(pool._ref, rows.data_ptr(), n, _stream(pool.device)))
+
+
+def pages_compact(pool: PagePool, remap=None, counts=None):
+    """Moves the pages in use to the front of the pool (ssd_pages_compact). Returns (remap
+    [n_pages] int32: each page's new number or -1, counts [2] int32: pages in use, moved)."""
+    dev = pool.device
+    remap = torch.empty(pool.n_pages, dtype=torch.int32, device=dev) if remap is None else remap
+    counts = torch.empty(2, dtype=torch.int32, device=dev) if counts is None else counts
+    _need(remap, "remap", (pool.n_pages,), torch.int32, dev)
+    _need(counts, "counts", (2,), torch.int32, dev)
+    with torch.cuda.device(dev):
+        _check(_lib.ssd_pages_compact(pool._ref, remap.data_ptr(), counts.data_ptr(), _stream(dev)))
+    return remap, counts
+
+
+def pages_copy(pool: PagePool, src, dst):
+    """Copies the bytes of pages src[i] into pages dst[i] in every array (ssd_pages_copy)."""
+    n = pool._list(src, "src")
+    pool._list(dst, "dst", n)
+    with torch.cuda.device(pool.device):
+        _check(_lib.ssd_pages_copy(pool._ref, src.data_ptr(), dst.data_ptr(), n, _stream(pool.device)))
