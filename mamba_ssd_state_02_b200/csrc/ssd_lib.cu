@@ -28,6 +28,7 @@
 #include "ssd_scan_simt.cuh"
 #include "ssd_strict.cuh"
 #include "ssd_scan_tc.cuh"
+#include "ssd_linattn_tc.cuh"
 #include "ssd_tc_selftest.cuh"
 
 namespace ssd {
@@ -1442,14 +1443,33 @@ ssd_status la_plan(const ssd_linear_attn_dims* d, bool varlen, LaPlan* out) {
     return SSD_OK;
 }
 
-template <typename T, bool OUT>
-ssd_status launch_la_simt(const LaPlan& p, int64_t segs, cudaStream_t st) {
-    const size_t smem = la::simt_smem(p.a.K, OUT);
-    cudaError_t e = cudaFuncSetAttribute(la::k_la_simt<T, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+// One pass over `segs` segments: the state each adds (OUT false), or the outputs.
+template <bool OUT>
+ssd_status launch_la(const LaPlan& p, int64_t segs, cudaStream_t st) {
+    const la::Args& a = p.a;
+    const unsigned grid = (unsigned)(segs * a.Hk * ((a.V + 63) / 64));
+    static_assert(la::kSimtV == 64 && la::kTcV == 64, "both kernels take 64 columns of V per CTA");
+    if (!p.bf16) {
+        const size_t smem = la::simt_smem(a.K, OUT);
+        cudaError_t e = cudaFuncSetAttribute(la::k_la_simt<OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(linear attention)");
+        StageScope sc(OUT ? ST_LA_SCAN : ST_LA_STATE, st);
+        la::k_la_simt<OUT><<<grid, la::kSimtThreads, smem, st>>>(a);
+        return SSD_OK;
+    }
+    CUtensorMap mq{}, mk{}, mv{};
+    const uint64_t T = (uint64_t)p.T;
+    if (T > 0 && (!make_map3(&mq, a.q, a.K, a.H, T, (uint64_t)a.K * 2, (uint64_t)a.q_stride * 2, 64, 1, la::kTcC) ||
+                  !make_map3(&mk, a.k, a.K, a.Hk, T, (uint64_t)a.K * 2, (uint64_t)a.k_stride * 2, 64, 1, la::kTcC) ||
+                  !make_map3(&mv, a.v, a.V, a.Hk, T, (uint64_t)a.V * 2, (uint64_t)a.v_stride * 2, 64, 1, la::kTcC)))
+        return fail(SSD_ERR_CUDA, "cuTensorMapEncodeTiled failed (q/k/v tensor maps)");
+    constexpr int smem = OUT ? la::kTcSmemOut : la::kTcSmemState;
+    cudaError_t e = cudaFuncSetAttribute(la::k_la_tc<OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(linear attention)");
-    const int nvb = (p.a.V + la::kSimtV - 1) / la::kSimtV;
+    la::Args b = a;
+    b.stall = g_test_stall.load() == (OUT ? 2 : 1);
     StageScope sc(OUT ? ST_LA_SCAN : ST_LA_STATE, st);
-    la::k_la_simt<T, OUT><<<(unsigned)(segs * p.a.Hk * nvb), la::kSimtThreads, smem, st>>>(p.a);
+    la::k_la_tc<OUT><<<grid, la::tc_threads(OUT), smem, st>>>(mq, mk, mv, b);
     return SSD_OK;
 }
 
@@ -1550,11 +1570,11 @@ extern "C" ssd_status ssd_linear_attn_fwd(const void* q, const void* k, const vo
     }
     if (two_pass) {
         const int64_t segs = cu_seqlens ? p.max_segs : (int64_t)a.nseq * (a.nps - 1);
-        s = p.bf16 ? launch_la_simt<__nv_bfloat16, false>(p, segs, st) : launch_la_simt<float, false>(p, segs, st);
+        s = launch_la<false>(p, segs, st);
         ++n;
     }
     if (s == SSD_OK) {
-        s = p.bf16 ? launch_la_simt<__nv_bfloat16, true>(p, p.max_segs, st) : launch_la_simt<float, true>(p, p.max_segs, st);
+        s = launch_la<true>(p, p.max_segs, st);
         ++n;
     }
     cudaError_t e = cudaGetLastError();

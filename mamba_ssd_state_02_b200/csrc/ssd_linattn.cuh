@@ -47,7 +47,7 @@ struct Args {
     int32_t nseq, nps;           // dense: segments per sequence
     int32_t Ls;                  // tokens per segment
     int32_t H, Hk, R, K, V;
-    int32_t stall;               // test hook: the tensor-core kernel's UMMA warp waits for nothing
+    int32_t stall;               // test hook: a wait of the tensor-core kernel's UMMA warp runs out
 };
 
 // One segment: tokens [start, start + len) of the packed rows, number j of the n segments
@@ -121,7 +121,8 @@ __device__ __forceinline__ void check_decay(float g) {
 }
 
 // ---------------------------------------------------------------------------------
-// CUDA-core prompt kernel (FP32 arithmetic throughout). One CTA per (segment, key/value
+// CUDA-core prompt kernel for fp32 (FP32 arithmetic throughout; the tensor cores would round
+// the inputs). One CTA per (segment, key/value
 // head, 64 columns of V); chunks of 64 tokens in shared memory; the state in shared
 // memory as [K][64]. Without OUT: only the state that the segment adds.
 constexpr int kSimtC = 64;           // tokens per chunk
@@ -134,7 +135,7 @@ __host__ __device__ constexpr size_t simt_smem(int K, bool out) {
                             (out ? kSimtC * (kSimtC + 4) : 0) + kSimtC + 4);
 }
 
-template <typename T, bool OUT>
+template <bool OUT>
 __global__ void __launch_bounds__(kSimtThreads) k_la_simt(const __grid_constant__ Args a) {
     constexpr int C = kSimtC, VB = kSimtV, NT = kSimtThreads;
     const int nvb = (a.V + VB - 1) / VB;
@@ -188,8 +189,8 @@ __global__ void __launch_bounds__(kSimtThreads) k_la_simt(const __grid_constant_
         sS[kk * VB + vv] = s;
     }
 
-    const T* kp = static_cast<const T*>(a.k) + sg.start * a.k_stride + (int64_t)g * K;
-    const T* vp = static_cast<const T*>(a.v) + sg.start * a.v_stride + (int64_t)g * V + v0;
+    const float* kp = static_cast<const float*>(a.k) + sg.start * a.k_stride + (int64_t)g * K;
+    const float* vp = static_cast<const float*>(a.v) + sg.start * a.v_stride + (int64_t)g * V + v0;
     const bool need_last = !OUT || fp >= 0;
     for (int c0 = 0; c0 < sg.len; c0 += C) {
         const int len = min(C, sg.len - c0);
@@ -207,7 +208,7 @@ __global__ void __launch_bounds__(kSimtThreads) k_la_simt(const __grid_constant_
         }
         if (OUT) {
             for (int r = 0; r < a.R; ++r) {
-                const T* qp = static_cast<const T*>(a.q) + (sg.start + c0) * a.q_stride + (int64_t)(g * a.R + r) * K;
+                const float* qp = static_cast<const float*>(a.q) + (sg.start + c0) * a.q_stride + (int64_t)(g * a.R + r) * K;
                 __syncthreads();             // readers of sq, sP are done
                 for (int e = tid; e < C * (K / 4); e += NT) {
                     const int t = e / (K / 4), c4 = e % (K / 4);
@@ -268,15 +269,16 @@ __global__ void __launch_bounds__(kSimtThreads) k_la_simt(const __grid_constant_
                         inter[i][3] = fmaf(x, y.w, inter[i][3]);
                     }
                 }
-                T* op = static_cast<T*>(a.o) + ((sg.start + c0) * a.H + g * a.R + r) * (int64_t)V + v0;
+                float* op = static_cast<float*>(a.o) + ((sg.start + c0) * a.H + g * a.R + r) * (int64_t)V + v0;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int t = ty + 16 * i;
                     if (t >= len || 4 * tx >= nv) continue;
                     const float w = pw[t + 1];
-                    T* p = op + (int64_t)t * a.H * V + 4 * tx;
+                    float y[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) p[j] = from_f32<T>(a.scale * fmaf(w, inter[i][j], acc[i][j]));
+                    for (int j = 0; j < 4; ++j) y[j] = a.scale * fmaf(w, inter[i][j], acc[i][j]);
+                    *reinterpret_cast<float4*>(op + (int64_t)t * a.H * V + 4 * tx) = make_float4(y[0], y[1], y[2], y[3]);
                 }
             }
         }
