@@ -1322,12 +1322,11 @@ struct LaPlan {
 };
 
 // Segment length in tokens (a multiple of 128). A pass's CTAs, one per (segment, key/value
-// head, 64 columns of V), run in waves of one per SM; a CTA costs its chunks plus about two
-// chunks of prologue and epilogue. More than one segment per sequence adds the state pass
-// (about half a chunk's cost per chunk, R query heads being nothing to it) and its launch
-// (about two chunks). Dense: the number of segments per sequence with the least cost.
-// Packed (lengths known on the device only): the same with the mean length, where the
-// longest segments are what the last wave waits for.
+// head, 64 columns of V), run in waves of one per SM; a CTA costs its chunks times the query
+// heads plus about two chunks of prologue and epilogue, in the state pass half a chunk per
+// chunk. Dense: the number of segments per sequence with the least cost. Packed (lengths known
+// on the device only): the same with the mean length, where the longest segments are what the
+// last wave waits for.
 int la_segment_tokens(const LaPlan& p) {
     constexpr int64_t kC = 128;
     const la::Args& a = p.a;
@@ -1339,9 +1338,8 @@ int la_segment_tokens(const LaPlan& p) {
         int64_t ls = nch;
         for (int64_t n = 1; n <= std::min<int64_t>(nch, 64); ++n) {
             const int64_t m = (nch + n - 1) / n, segs = (nch + m - 1) / m;
-            auto waves = [&](int64_t s) { return (double)((a.nseq * s * heads + nsm - 1) / nsm); };
-            double c = waves(segs) * (double)(m * a.R + 2);
-            if (segs > 1) c += waves(segs - 1) * (0.5 * (double)m + 2) + 2;
+            const double waves = (double)((a.nseq * segs * heads + nsm - 1) / nsm);
+            const double c = waves * (double)(m * a.R + 2) + waves * (0.5 * (double)m + 2);
             if (n == 1 || c < best) {
                 best = c;
                 ls = m;
@@ -1353,9 +1351,8 @@ int la_segment_tokens(const LaPlan& p) {
     double best = 0;
     int64_t ls = 2;
     for (int64_t m = 2; m <= 8192; m *= 2) {
-        const double frac = std::max(0.0, 1.0 - (double)m / (2 * mean));
-        const double c = U * a.R + (double)(std::min<double>(m, 2 * mean) * a.R) + 0.5 * (U * frac + (frac > 0 ? m : 0)) +
-                         2 * U / std::min<double>(m, mean) + (frac > 0 ? 4 : 0);
+        const double longest = std::min<double>((double)m, 2 * mean), cost = a.R + 0.5;
+        const double c = U * cost + longest * cost + 4 * U / std::min<double>((double)m, mean);
         if (m == 2 || c < best) {
             best = c;
             ls = m;
@@ -1437,8 +1434,10 @@ ssd_status la_plan(const ssd_linear_attn_dims* d, bool varlen, LaPlan* out) {
         p.off_count = take(sizeof(int32_t));
         p.off_order = take(sizeof(int32_t) * n);
     }
-    // Without a second segment anywhere no slot is used.
-    if (varlen ? p.T > a.Ls : a.nps > 1) p.off_slots = take(sizeof(float) * (size_t)p.max_segs * a.Hk * a.V * a.K);
+    // A state slot per segment and one per sequence. Without a second segment anywhere the
+    // CUDA-core kernel uses none.
+    if (p.bf16 || (varlen ? p.T > a.Ls : a.nps > 1))
+        p.off_slots = take(sizeof(float) * (size_t)(p.max_segs + a.nseq) * a.Hk * a.V * a.K);
     p.bytes = std::max<size_t>(off, 256);
     return SSD_OK;
 }
@@ -1459,17 +1458,23 @@ ssd_status launch_la(const LaPlan& p, int64_t segs, cudaStream_t st) {
     }
     CUtensorMap mq{}, mk{}, mv{};
     const uint64_t T = (uint64_t)p.T;
-    if (T > 0 && (!make_map3(&mq, a.q, a.K, a.H, T, (uint64_t)a.K * 2, (uint64_t)a.q_stride * 2, 64, 1, la::kTcC) ||
+    if (T > 0 && ((OUT && !make_map3(&mq, a.q, a.K, a.H, T, (uint64_t)a.K * 2, (uint64_t)a.q_stride * 2, 64, 1, la::kTcC)) ||
                   !make_map3(&mk, a.k, a.K, a.Hk, T, (uint64_t)a.K * 2, (uint64_t)a.k_stride * 2, 64, 1, la::kTcC) ||
                   !make_map3(&mv, a.v, a.V, a.Hk, T, (uint64_t)a.V * 2, (uint64_t)a.v_stride * 2, 64, 1, la::kTcC)))
         return fail(SSD_ERR_CUDA, "cuTensorMapEncodeTiled failed (q/k/v tensor maps)");
-    constexpr int smem = OUT ? la::kTcSmemOut : la::kTcSmemState;
-    cudaError_t e = cudaFuncSetAttribute(la::k_la_tc<OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(linear attention)");
     la::Args b = a;
     b.stall = g_test_stall.load() == (OUT ? 2 : 1);
-    StageScope sc(OUT ? ST_LA_SCAN : ST_LA_STATE, st);
-    la::k_la_tc<OUT><<<grid, la::tc_threads(OUT), smem, st>>>(mq, mk, mv, b);
+    if (OUT) {
+        cudaError_t e = cudaFuncSetAttribute(la::k_la_tc_out, cudaFuncAttributeMaxDynamicSharedMemorySize, la::kOutSmem);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(linear attention)");
+        StageScope sc(ST_LA_SCAN, st);
+        la::k_la_tc_out<<<grid, la::kOutThreads, la::kOutSmem, st>>>(mq, mk, mv, b);
+    } else {
+        cudaError_t e = cudaFuncSetAttribute(la::k_la_tc_state, cudaFuncAttributeMaxDynamicSharedMemorySize, la::kStateSmem);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(linear attention)");
+        StageScope sc(ST_LA_STATE, st);
+        la::k_la_tc_state<<<grid, la::kStateThreads, la::kStateSmem, st>>>(mk, mv, b);
+    }
     return SSD_OK;
 }
 
@@ -1530,7 +1535,8 @@ extern "C" ssd_status ssd_linear_attn_fwd(const void* q, const void* k, const vo
         return SSD_OK;
     }
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const bool two_pass = cu_seqlens ? p.T > a.Ls : a.nps > 1;
+    // The tensor-core output pass needs the state pass for a final state too.
+    const bool many = cu_seqlens ? p.T > a.Ls : a.nps > 1, two_pass = many || (p.bf16 && final_state);
     char* ws = static_cast<char*>(dims->workspace);
     bool owned = false;
     if (ws) {
@@ -1553,6 +1559,7 @@ extern "C" ssd_status ssd_linear_attn_fwd(const void* q, const void* k, const vo
     a.fin_pages = final_pages;
     a.o = o;
     a.slots = reinterpret_cast<float*>(ws + p.off_slots);
+    a.two_pass = two_pass;
     int n = 0;
     if (cu_seqlens) {
         auto* table = reinterpret_cast<ChunkEntry*>(ws + p.off_table);
@@ -1569,7 +1576,7 @@ extern "C" ssd_status ssd_linear_attn_fwd(const void* q, const void* k, const vo
         ++n;
     }
     if (two_pass) {
-        const int64_t segs = cu_seqlens ? p.max_segs : (int64_t)a.nseq * (a.nps - 1);
+        const int64_t segs = cu_seqlens || p.bf16 ? p.max_segs : (int64_t)a.nseq * (a.nps - 1);
         s = launch_la<false>(p, segs, st);
         ++n;
     }

@@ -47,11 +47,12 @@ struct Args {
     int32_t nseq, nps;           // dense: segments per sequence
     int32_t Ls;                  // tokens per segment
     int32_t H, Hk, R, K, V;
-    int32_t stall;               // test hook: a wait of the tensor-core kernel's UMMA warp runs out
+    bool two_pass;               // a state pass ran before the output pass
+    bool stall;                  // test hook: a wait of the tensor-core kernel's UMMA warp runs out
 };
 
 // One segment: tokens [start, start + len) of the packed rows, number j of the n segments
-// of sequence seq, whose state slots begin at slot0. Slot slot0 holds a copy of the
+// of sequence seq, whose n + 1 state slots begin at slot0. Slot slot0 holds a copy of the
 // sequence's initial state (the state may be replaced in place while other segments'
 // CTAs still run), slot0 + i the state that segment i-1 alone adds.
 struct Seg {
@@ -59,26 +60,26 @@ struct Seg {
     int64_t start;
 };
 
-// Segment `i` of a pass; false where a packed call has fewer. A state pass (OUT false)
-// has no CTAs for a dense sequence's last segment, and its packed CTAs of one return.
-template <bool OUT>
-__device__ __forceinline__ bool find_seg(const Args& a, int i, Seg* s) {
+// Segment `i` of a pass; false where a packed call has fewer. `last`: the pass takes each
+// sequence's last segment too.
+__device__ __forceinline__ bool find_seg(const Args& a, int i, bool last, Seg* s) {
     if (a.table) {
         if (i >= *a.count) return false;
         const ChunkEntry e = a.table[a.order[i]];
         s->seq = e.seq;
         s->start = e.start;
         s->len = e.len;
-        s->slot0 = a.first[e.seq];
-        s->n = a.first[e.seq + 1] - s->slot0;
-        s->j = e.pad - s->slot0;
-        return OUT || s->j + 1 < s->n;
+        const int first = a.first[e.seq];
+        s->slot0 = first + e.seq;
+        s->n = a.first[e.seq + 1] - first;
+        s->j = e.pad - first;
+        return last || s->j + 1 < s->n;
     }
-    const int per = OUT ? a.nps : a.nps - 1;
+    const int per = last ? a.nps : a.nps - 1;
     s->seq = i / per;
     s->j = i % per;
     s->n = a.nps;
-    s->slot0 = s->seq * a.nps;
+    s->slot0 = s->seq * (a.nps + 1);
     s->start = (int64_t)s->seq * a.seqlen + (int64_t)s->j * a.Ls;
     s->len = (int32_t)min((int64_t)a.Ls, a.seqlen - (int64_t)s->j * a.Ls);
     return true;
@@ -109,9 +110,13 @@ __device__ __forceinline__ bool page_clash(const Args& a, int32_t s, int64_t p, 
     return __syncthreads_or(bad) != 0;
 }
 
+// lam^n in 64 bits. Not inlined: the prompt kernels take it at six places, and code that runs
+// once per CTA should not crowd the instruction cache.
+__device__ __noinline__ double pow_decay(float g, int64_t n) { return exp((double)g * (double)n); }
+
 // lam^n as hi + lo; hi is lam^n rounded to float.
-__device__ __forceinline__ float2 pow2f(double g, int64_t n) {
-    const double e = exp(g * (double)n);
+__device__ __forceinline__ float2 pow2f(float g, int64_t n) {
+    const double e = pow_decay(g, n);
     const float hi = (float)e;
     return make_float2(hi, (float)(e - (double)hi));
 }
@@ -141,7 +146,7 @@ __global__ void __launch_bounds__(kSimtThreads) k_la_simt(const __grid_constant_
     const int nvb = (a.V + VB - 1) / VB;
     const int vb = blockIdx.x % nvb, g = (blockIdx.x / nvb) % a.Hk;
     Seg sg;
-    if (!find_seg<OUT>(a, blockIdx.x / nvb / a.Hk, &sg)) return;
+    if (!find_seg(a, blockIdx.x / nvb / a.Hk, OUT, &sg)) return;
     const int K = a.K, V = a.V, ldk = simt_ld(K), tid = threadIdx.x;
     const int v0 = vb * VB, nv = min(VB, V - v0);
 
@@ -155,7 +160,7 @@ __global__ void __launch_bounds__(kSimtThreads) k_la_simt(const __grid_constant_
     __shared__ float2 lam_seg;
 
     const float gd = a.log_decay[g];
-    if (tid <= C) pw[tid] = (float)exp((double)gd * tid);
+    if (tid <= C) pw[tid] = (float)pow_decay(gd, tid);
     if (tid == 0) {
         check_decay(gd);
         lam_seg = pow2f(gd, a.Ls);
