@@ -87,7 +87,7 @@ __device__ __forceinline__ bool find_seg(const Args& a, int i, bool last, Seg* s
 
 // Where sequence s's state is in an array of states: its page, or s without a page list.
 // -1 stands for "none"; a page outside the pool is an error and stands for none too.
-__device__ __forceinline__ int64_t page_of(const int32_t* pages, int64_t npages, int32_t s) {
+__device__ __noinline__ int64_t page_of(const int32_t* pages, int64_t npages, int32_t s) {
     if (!pages) return s;
     const int32_t p = pages[s];
     if (p < -1 || p >= npages) {
@@ -99,7 +99,7 @@ __device__ __forceinline__ int64_t page_of(const int32_t* pages, int64_t npages,
 
 // Whether sequence s must not write its final state to page p: an earlier sequence writes
 // the same page, or another one starts from it in this call. Called by the whole block.
-__device__ __forceinline__ bool page_clash(const Args& a, int32_t s, int64_t p, int threads) {
+__device__ __noinline__ bool page_clash(const Args& a, int32_t s, int64_t p, int threads) {
     int bad = 0;
     const bool one_pool = a.init == a.fin;
     for (int32_t i = threadIdx.x; i < a.nseq; i += threads) {

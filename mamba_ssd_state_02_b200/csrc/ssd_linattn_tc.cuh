@@ -38,32 +38,26 @@ constexpr int kTcV = 64;                     // V columns per CTA
 constexpr int kBlock = 32;                   // columns of a score block
 constexpr int kStateWarps = 8;
 
-// Where a state column of a thread lies: element (v, k) of a [V][K] state at v * K + k; the
-// thread has k fixed and up to 32 consecutive v, lanes side by side along K.
-struct Column {
-    int offset, rows, K;
-    __device__ __forceinline__ Column(int k, int first_v, int nv, int K_)
-        : offset(first_v * K_ + k), rows(k < K_ ? max(0, min(32, nv - first_v)) : 0), K(K_) {}
-};
-
-// S = x (FIRST), or lam S + x, for the column x at p. Eight loads at a time: all 32 with their
-// addresses would not fit in registers next to S.
-template <bool FIRST>
-__device__ __forceinline__ void take(float (&S)[32], const Column& c, const float* p, float2 lam) {
-    p += c.offset;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        float x[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i, p += c.K) x[i] = 8 * e + i < c.rows ? *p : 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float& s = S[8 * e + i];
-            s = FIRST ? x[i] : fmaf(lam.x, s, fmaf(lam.y, s, x[i]));
+// Bounded waits, as wait_abort and wait_issue of the scan's passes (an expired wait latches
+// SSD_ERR_TIMEOUT and raises the CTA's abort flag, after which every wait returns; the issuing
+// warps look at the flag after their waits and stop), but short: the passes have two dozen
+// waits in loops that ten warps with code of their own run at once, and their code has to
+// stay within the instruction cache (at twice the size the output pass took 1.25 times as
+// long). The budget is 4e9 cycles of the 32-bit clock.
+__device__ __forceinline__ void wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    if (tc::mbar_try_wait_sleep(bar, parity & 1)) return;
+    const uint32_t t0 = (uint32_t)clock();
+    while (!tc::mbar_try_wait_sleep(bar, parity & 1)) {
+        if (*abort_flag) return;
+        if ((uint32_t)clock() - t0 > 4000000000u) {
+            latch_error(SSD_ERR_TIMEOUT);
+            *abort_flag = 1;
         }
-        __syncwarp();
     }
 }
+
+// For an issuing warp, after its waits: none of them was given up.
+__device__ __forceinline__ bool go_on(volatile int* abort_flag) { return __all_sync(0xffffffffu, *abort_flag == 0); }
 
 // Row `r` (0..127), 16-byte chunk `c` of a [128][64] bf16 tile in the 128-byte swizzle.
 __device__ __forceinline__ uint32_t tile_at(uint32_t base, int r, int c) { return base + tc::swz(r, c); }
@@ -96,7 +90,9 @@ k_la_tc_state(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ float pw[kTcC + 1];
     __shared__ float2 lam_full, lam_tail;
-    __shared__ uint64_t full[2], done[2], w_ready[2], d_free[2], drained, stall_bar;
+    __shared__ uint64_t bars[10];
+    uint64_t *full = bars, *done = bars + 2, *w_ready = bars + 4, *d_free = bars + 6;
+    uint64_t &drained = bars[8], &stall_bar = bars[9];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
 
@@ -105,19 +101,12 @@ k_la_tc_state(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
     if (tid <= kTcC) pw[tid] = (float)pow_decay(gd, tid);
     if (tid == 160) lam_full = pow2f(gd, kTcC);
     if (tid == 192) lam_tail = pow2f(gd, nt > 0 ? len_of(nt - 1) : 0);
+    if (tid < 10) mbar_init(&bars[tid], tid == 4 || tid == 5 ? kWriteWarps : tid == 6 || tid == 7 ? kStateWarps : 1);
     if (tid == 0) {
         check_decay(gd);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&done[i], 1);
-            mbar_init(&w_ready[i], kWriteWarps);
-            mbar_init(&d_free[i], kStateWarps);
-        }
-        mbar_init(&drained, 1);
-        mbar_init(&stall_bar, 1);
         abort_flag = 0;
-        fence_barrier_init();
     }
+    fence_barrier_init();
     if (warp == 1) {
         tmem_alloc(&tmem_slot, 512);
         tmem_relinquish();
@@ -143,7 +132,8 @@ k_la_tc_state(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
                     for (int h = 0; h < halves; ++h) tma_prefetch_3d(&map_k, 64 * h, g, t0 + kTcC);
                     tma_prefetch_3d(&map_v, v0, g, t0 + kTcC);
                 }
-                if (c >= 2 && !wait_issue(&done[b], ((c >> 1) - 1) & 1, abort_p)) break;
+                if (c >= 2) wait_bar(&done[b], (c >> 1) - 1, abort_p);
+                if (*abort_p) break;
                 mbar_arrive_expect_tx(&full[b], (halves + 1) * 16384);
 #pragma unroll 1
                 for (int h = 0; h < halves; ++h) tma_load_3d(sm + b * 32768 + h * 16384, &map_k, &full[b], 64 * h, g, t0);
@@ -160,13 +150,14 @@ k_la_tc_state(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
         // D (k x [v hi | v mid | v lo]) = K^T (w V): A = K, MN-major; B = w V, MN-major.
         const uint32_t id = idesc_bf16(128, 192, 1, 1);
         const uint64_t dK = smem_desc(smem_u32(sm), 16384, 1024), dW = smem_desc(smem_u32(sm + kStateW), 16384, 1024);
-        bool ok = !(a.stall && !wait_issue_warp(&stall_bar, 0, abort_p));     // test hook: a wait that runs out
+        if (a.stall) wait_bar(&stall_bar, 0, abort_p);            // test hook: a wait that runs out
 #pragma unroll 1
-        for (int c = 0; c < nt && ok; ++c) {
-            const int b = c & 1, ph = (c >> 1) & 1;
-            if (!wait_issue_warp(&full[b], ph, abort_p) || !wait_issue_warp(&w_ready[b], ph, abort_p) ||
-                (c >= 2 && !wait_issue_warp(&d_free[b], ph ^ 1, abort_p)))
-                break;
+        for (int c = 0; c < nt; ++c) {
+            const int b = c & 1, ph = c >> 1;
+            wait_bar(&full[b], ph, abort_p);
+            wait_bar(&w_ready[b], ph, abort_p);
+            if (c >= 2) wait_bar(&d_free[b], ph - 1, abort_p);
+            if (!go_on(abort_p)) break;
             tc_fence_after();
             const uint64_t dk = desc_add(dK, b * 32768), dw = desc_add(dW, b * 49152);
             const uint32_t d = tD + 256 * b;
@@ -192,8 +183,8 @@ k_la_tc_state(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
 #pragma unroll 1
         for (int c = 0; c < nt; ++c) {
             const int b = c & 1, len = len_of(c), rows = 16 * steps_of(c);
-            wait_abort(&full[b], (c >> 1) & 1, abort_p);
-            if (c >= 2) wait_abort(&done[b], ((c >> 1) - 1) & 1, abort_p);
+            wait_bar(&full[b], (c >> 1) & 1, abort_p);
+            if (c >= 2) wait_bar(&done[b], ((c >> 1) - 1) & 1, abort_p);
             const uint32_t sv = smem_u32(sm + kStateV) + b * 16384, sw = smem_u32(sm + kStateW) + b * 49152;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -232,27 +223,24 @@ k_la_tc_state(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
     } else {
         // ------------------------------------------------------------ the state
         // Thread: state row k = 32 quarter + lane, 32 of the 64 V columns.
-        const int quarter = warp & 3, half = (warp - 4 - kWriteWarps) >> 2;
-        const Column col(32 * quarter + lane, 32 * half, nv, K);
+        const int quarter = warp & 3, half = (warp - 4 - kWriteWarps) >> 2, k = 32 * quarter + lane;
         float* slots = a.slots + (int64_t)sg.slot0 * per_state + head;
-        float S[32];
         if (sg.j == 0 && a.init) {
             // The output pass starts from a copy: the final state may replace the initial one.
             const int64_t ip = page_of(a.init_pages, a.npages, sg.seq);
             if (ip >= 0) {
-                take<true>(S, col, a.init + ip * per_state + head, make_float2(0.f, 0.f));
-                float* p = slots + col.offset;
-#pragma unroll
-                for (int i = 0; i < 32; ++i, p += K)
-                    if (i < col.rows) *p = S[i];
+                const float* from = a.init + ip * per_state + head;
+#pragma unroll 4
+                for (int e = tid - 32 * (4 + kWriteWarps); e < nv * K; e += 32 * kStateWarps) slots[e] = from[e];
             }
         }
+        float S[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) S[i] = 0.f;
 #pragma unroll 1
         for (int c = 0; c < nt; ++c) {
             const int b = c & 1;
-            wait_abort(&done[b], (c >> 1) & 1, abort_p);
+            wait_bar(&done[b], (c >> 1) & 1, abort_p);
             tc_fence_after();
             const uint32_t t = tD + 256 * b + ((uint32_t)quarter << 21) + 32 * half;
             const float2 lam = c == nt - 1 ? lam_tail : lam_full;
@@ -275,10 +263,12 @@ k_la_tc_state(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
                 }
             }
         }
-        float* p = slots + (int64_t)(sg.j + 1) * per_state + col.offset;
+        // lanes side by side along K
+        float* p = slots + (int64_t)(sg.j + 1) * per_state + 32 * half * K + k;
+        const int rows = k < K ? nv - 32 * half : 0;
 #pragma unroll
         for (int i = 0; i < 32; ++i, p += K)
-            if (i < col.rows) *p = S[i];
+            if (i < rows) *p = S[i];
     }
     tc_fence_before();
     __syncthreads();
@@ -286,21 +276,32 @@ k_la_tc_state(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
 }
 
 // ---------------------------------------------------------------------------------
-// Output pass. Warp 0 issues the TMA loads, warp 1 the UMMAs of P, Oi and Ox, warp 2 those of
-// the state (an issuing warp takes its batches in order, and the state's waits would hold up
-// the outputs'); then three groups of eight warps: scores, outputs, and w V with the state.
-// Q, K and V are double-buffered, and what they have no room for yet is brought into L2.
+// Output pass. Warp 0 issues the TMA loads; warp 3 the UMMAs of Q K^T, warp 1 those of Oi and
+// Ox, warp 2 those of D (an issuing warp takes its batches in order, and the waits of one
+// product would hold up the others); then three groups of eight warps: scores and w V, outputs,
+// and the state. Q, K and V are double-buffered, and what they have no room for yet is brought
+// into L2. Q K^T runs one unit ahead, in the gap that the outputs leave in the tensor pipe
+// while they are read.
 //
 // Shared memory: K, V, Q (two buffers each), S (a bf16 pair), w V. TMEM columns: Q K^T [0, 128)
 // and [128, 256) (units alternate), P of a 32-token block in the first 16 columns of the
 // block's scores (read and written by the same thread), Oi [256, 320), Ox [320, 448), D
 // [448, 512).
 
-// Registers of the calling group of four warps, all of which execute it.
-template <int N>
-__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+// A matrix descriptor's low word: start address, and the distance between 64-wide blocks of an
+// MN-major operand (16 KB; not read for K-major ones). The high word is the same for all. In
+// units of 16 bytes, a K-step of 16 advances a K-major operand by 2, the other half of its
+// columns lies 1024 on, and a K-step of an MN-major operand is 128.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return (saddr >> 4) | (16384u >> 4) << 16; }
+constexpr uint32_t kDescHi = (1024 >> 4) | 1u << 14 | 2u << 29;          // SBO, version, 128-byte swizzle
+
+__device__ __forceinline__ void umma(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool accumulate) {
+    const uint64_t hi = (uint64_t)kDescHi << 32;
+    tc::umma_bf16(d, hi | a_lo, hi | b_lo, idesc, accumulate);
+}
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, bool accumulate) {
+    tc::umma_bf16_ts(d, a_tmem, (uint64_t)kDescHi << 32 | b_lo, idesc, accumulate);
+}
 
 constexpr int kScoreWarps = 8, kOutWarps = 8;
 constexpr int kOutThreads = 32 * (4 + kScoreWarps + kOutWarps + kStateWarps);
@@ -316,7 +317,7 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
     Seg sg;
     if (!find_seg(a, blockIdx.x / nvb / a.Hk, true, &sg)) return;
     const int K = a.K, R = a.R, v0 = vb * kTcV, nv = min(kTcV, a.V - v0);
-    const int nt = (sg.len + kTcC - 1) / kTcC, ksteps = (K + 15) / 16, halves = (K + 63) / 64;
+    const int nt = (sg.len + kTcC - 1) / kTcC, halves = (K + 63) / 64;
     const bool partial = sg.len % kTcC != 0;                      // the last chunk
     auto len_of = [&](int c) { return min(kTcC, sg.len - c * kTcC); };
     auto blocks_of = [&](int c) { return (len_of(c) + kBlock - 1) / kBlock; };
@@ -324,10 +325,11 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ float pw_pad[32 + kTcC + 1];  // 32 zeros, then lam^0 .. lam^128
-    __shared__ __align__(16) float rev[32];  // lam^31 .. lam^0
     __shared__ float2 lam_full, lam_seg, lam_len;
-    __shared__ uint64_t full_k[2], empty_k[2], full_v[2], empty_v[2], full_q[2], empty_q[2], qk_done[2], p_ready[2],
-        o_done, o_free, qs_done, w_ready, d_done, s_ready, tail_ready, drained[2], stall_bar;
+    // pairs for the two buffers of K, V, Q and the scores, then single barriers
+    enum { FULL_K = 0, EMPTY_K = 2, FULL_V = 4, EMPTY_V = 6, FULL_Q = 8, EMPTY_Q = 10, QK_DONE = 12, P_READY = 14, O_DONE = 16,
+           O_FREE = 18, QS_DONE, W_READY, D_DONE, D_FREE, S_READY, TAIL_READY, DRAINED, STALL = DRAINED + 3, BARS };
+    __shared__ uint64_t bars[BARS];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     const float* pw = pw_pad + 32;
@@ -335,34 +337,20 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const float gd = a.log_decay[g];
     if (tid < 32 + kTcC + 1) pw_pad[tid] = tid < 32 ? 0.f : (float)pow_decay(gd, tid - 32);
-    if (tid >= 192 && tid < 224) rev[tid - 192] = (float)pow_decay(gd, 31 - (tid - 192));
     if (tid == 256) lam_full = pow2f(gd, kTcC);
     if (tid == 288) lam_seg = pow2f(gd, a.Ls);
     if (tid == 320) lam_len = pow2f(gd, sg.len);
+    if (tid < BARS) {
+        const int pair = tid & ~1;
+        mbar_init(&bars[tid], pair == EMPTY_K || pair == EMPTY_V || pair == EMPTY_Q ? 2
+                              : pair == P_READY || tid == O_FREE || (tid >= D_FREE && tid <= TAIL_READY) || tid == W_READY ? 8 : 1);
+    }
+    static_assert(kScoreWarps == 8 && kOutWarps == 8 && kStateWarps == 8, "arrivals a group makes on a barrier");
     if (tid == 0) {
         check_decay(gd);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&full_k[i], 1);
-            mbar_init(&empty_k[i], 2);
-            mbar_init(&full_v[i], 1);
-            mbar_init(&empty_v[i], 2);
-            mbar_init(&full_q[i], 1);
-            mbar_init(&empty_q[i], 1);
-            mbar_init(&qk_done[i], 1);
-            mbar_init(&p_ready[i], kScoreWarps);
-            mbar_init(&drained[i], 1);
-        }
-        mbar_init(&o_done, 1);
-        mbar_init(&o_free, kOutWarps);
-        mbar_init(&qs_done, 1);
-        mbar_init(&w_ready, kStateWarps);
-        mbar_init(&d_done, 1);
-        mbar_init(&s_ready, kStateWarps);
-        mbar_init(&tail_ready, kStateWarps);
-        mbar_init(&stall_bar, 1);
         abort_flag = 0;
-        fence_barrier_init();
     }
+    fence_barrier_init();
     if (warp == 1) {
         tmem_alloc(&tmem_slot, 512);
         tmem_relinquish();
@@ -384,174 +372,206 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
     volatile int* abort_p = &abort_flag;
     const bool has_init = ip >= 0 || sg.j > 0;                    // the first chunk meets a state
 
-    // Registers: 72 a thread at launch (896 threads), moved between groups of four warps:
-    // 56 + 2 * 72 + 2 * 72 + 2 * 80 = 7 * 72.
     if (warp == 0) {
         // ------------------------------------------------------------ TMA producer
-        regs_dec<56>();
+        // Per chunk: K, the first Q, V, the other Qs; every load waits until its buffer is free,
+        // and brings the tile two turns of the buffers on into L2.
         if (lane == 0 && nt > 0) {
-            prefetch_tmap(&map_k);
-            prefetch_tmap(&map_v);
-            prefetch_tmap(&map_q);
-            int nk = 0, nl = 0, nq = 0;      // loads of K, V and Q issued (alternating buffers)
-            auto row = [&](int c) { return (int)(sg.start + (int64_t)c * kTcC); };
-            auto load_q = [&](int c, int r) -> bool {
-                const int u = c * R + r, b = u & 1;
-                if (u >= 2 && !wait_issue(&empty_q[b], ((u >> 1) - 1) & 1, abort_p)) return false;
-                mbar_arrive_expect_tx(&full_q[b], halves * 16384);
+            int c = 0, r = 0, job = 0, n[3] = {0, 0, 0};          // loads of K, V and Q issued
 #pragma unroll 1
-                for (int h = 0; h < halves; ++h)
-                    tma_load_3d(sm + kOutQ + b * 32768 + h * 16384, &map_q, &full_q[b], 64 * h, g * R + r, row(c));
-                ++nq;
-                const int r2 = (r + 2) % R, c2 = c + (r + 2) / R;             // two units on, into L2
-                if (c2 < nt)
-#pragma unroll 1
-                    for (int h = 0; h < halves; ++h) tma_prefetch_3d(&map_q, 64 * h, g * R + r2, row(c2));
-                return true;
-            };
-            bool ok = true;
-#pragma unroll 1
-            for (int c = 0; c < nt && ok; ++c) {
-                const int b = c & 1;
-                if (c >= 2 && !wait_issue(&empty_k[b], ((c >> 1) - 1) & 1, abort_p)) break;
-                mbar_arrive_expect_tx(&full_k[b], halves * 16384);
-#pragma unroll 1
-                for (int h = 0; h < halves; ++h)
-                    tma_load_3d(sm + b * 32768 + h * 16384, &map_k, &full_k[b], 64 * h, g, row(c));
-                ++nk;
-                if (!load_q(c, 0)) break;
-                if (c >= 2 && !wait_issue(&empty_v[b], ((c >> 1) - 1) & 1, abort_p)) break;
-                mbar_arrive_expect_tx(&full_v[b], 16384);
-                tma_load_3d(sm + kOutV + b * 16384, &map_v, &full_v[b], v0, g, row(c));
-                ++nl;
-                if (c + 2 < nt) {            // two chunks on, into L2
-#pragma unroll 1
-                    for (int h = 0; h < halves; ++h) tma_prefetch_3d(&map_k, 64 * h, g, row(c + 2));
-                    tma_prefetch_3d(&map_v, v0, g, row(c + 2));
+            while (c < nt && !*abort_p) {
+                const bool k_ = job == 0, v_ = job == 2;
+                const int i = k_ ? n[0] : v_ ? n[1] : n[2], b = i & 1, tiles = v_ ? 1 : halves;
+                const CUtensorMap* map = k_ ? &map_k : v_ ? &map_v : &map_q;
+                uint64_t* full = &bars[(k_ ? FULL_K : v_ ? FULL_V : FULL_Q) + b];
+                uint8_t* dst = sm + (k_ ? b * 32768 : v_ ? kOutV + b * 16384 : kOutQ + b * 32768);
+                const int x = v_ ? v0 : 0, head_ = k_ || v_ ? g : g * R + r;
+                const int ahead = k_ || v_ ? c + 2 : R == 1 ? c + 2 : r + 2 < R ? c : c + 1;
+                const int head2 = k_ || v_ || R == 1 ? head_ : r + 2 < R ? head_ + 2 : head_ + 2 - R;
+                if (i >= 2) {
+                    wait_bar(full + 2, (i >> 1) - 1, abort_p);    // EMPTY follows FULL
+                    if (*abort_p) break;
                 }
+                mbar_arrive_expect_tx(full, tiles * 16384);
 #pragma unroll 1
-                for (int r = 1; r < R && ok; ++r) ok = load_q(c, r);
+                for (int t = 0; t < tiles; ++t) {
+                    tma_load_3d(dst + t * 16384, map, full, x + 64 * t, head_, (int)(sg.start + (int64_t)c * kTcC));
+                    if (ahead < nt) tma_prefetch_3d(map, x + 64 * t, head2, (int)(sg.start + (int64_t)ahead * kTcC));
+                }
+                if (k_) ++n[0]; else if (v_) ++n[1]; else { ++n[2]; ++r; }
+                if (++job == R + 2) {
+                    job = r = 0;
+                    ++c;
+                }
             }
             // As in the state pass: wait for what is in flight.
-            for (int i = 0; i < 2; ++i) {
-                if (nk > i) mbar_wait(&full_k[i], ((nk - 1 - i) >> 1) & 1);
-                if (nl > i) mbar_wait(&full_v[i], ((nl - 1 - i) >> 1) & 1);
-                if (nq > i) mbar_wait(&full_q[i], ((nq - 1 - i) >> 1) & 1);
-            }
-        }
-    } else if (warp == 1) {
-        // ------------------------------------------------------------ UMMA issuer: P, Oi, Ox
-        regs_dec<56>();
-        const uint32_t id_x = idesc_bf16(128, 128, 0, 1), id_v = idesc_bf16(128, 64, 0, 1);
-        const uint64_t dQ = smem_desc(smem_u32(sm + kOutQ), 16, 1024), dK = smem_desc(smem_u32(sm), 16, 1024);
-        const uint64_t dV = smem_desc(smem_u32(sm + kOutV), 16384, 1024), dS = smem_desc(smem_u32(sm + kOutS), 16384, 1024);
-        // Q K^T of unit u = (c, r): N = the chunk's tokens rounded up to a block.
-        auto issue_qk = [&](int c, int r, int u) -> bool {
-            if (r == 0 && !wait_issue_warp(&full_k[c & 1], (c >> 1) & 1, abort_p)) return false;
-            if (!wait_issue_warp(&full_q[u & 1], (u >> 1) & 1, abort_p)) return false;
-            tc_fence_after();
-            const uint32_t id = idesc_bf16(128, kBlock * blocks_of(c), 0, 0), d = tbase + 128 * (u & 1);
-            const uint64_t dq = desc_add(dQ, (u & 1) * 32768), dk = desc_add(dK, (c & 1) * 32768);
-            if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (k < ksteps)
-                        umma_bf16(d, desc_add(dq, kmajor_step(128, k)), desc_add(dk, kmajor_step(128, k)), id, k > 0);
-                umma_commit(&qk_done[u & 1]);
-                if (r == R - 1) umma_commit(&empty_k[c & 1]);
-            }
-            __syncwarp();
-            return true;
-        };
-        // test hook (stall): a wait that runs out
-        bool ok = nt > 0 && !(a.stall && !wait_issue_warp(&stall_bar, 0, abort_p)) && issue_qk(0, 0, 0);
+            for (int m = 0; m < 3; ++m)
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+                    if (n[m] > b) mbar_wait(&bars[4 * m + b], ((n[m] - 1 - b) >> 1) & 1);
+        }
+    } else if (warp == 3) {
+        // ------------------------------------------------------------ UMMA issuer: Q K^T
+        const uint32_t dQ = desc_lo(smem_u32(sm + kOutQ)), dK = desc_lo(smem_u32(sm));
+        bool ok = true;
         int u = 0;
 #pragma unroll 1
         for (int c = 0; c < nt && ok; ++c) {
-            const bool st = c > 0 || has_init;
+            const uint32_t id = idesc_bf16(128, kBlock * blocks_of(c), 0, 0);          // N: whole blocks
+            const uint32_t dk = dK + (c & 1) * 2048;
 #pragma unroll 1
             for (int r = 0; r < R; ++r, ++u) {
-                ok = (u == 0 || wait_issue_warp(&o_free, (u - 1) & 1, abort_p)) &&
-                     (!st || r > 0 || wait_issue_warp(&s_ready, (has_init ? c : c - 1) & 1, abort_p));
-                if (!ok) break;
+                // The buffer last held P of unit u-2, whose product is done.
+                if (u >= 2) wait_bar(&bars[O_DONE + (u & 1)], (u >> 1) - 1, abort_p);
+                if (r == 0) wait_bar(&bars[FULL_K + (c & 1)], c >> 1, abort_p);
+                wait_bar(&bars[FULL_Q + (u & 1)], u >> 1, abort_p);
+                if (!(ok = go_on(abort_p))) break;
                 tc_fence_after();
-                const uint64_t dq = desc_add(dQ, (u & 1) * 32768);
-                const int xsteps = st ? ksteps : 0;
+                const uint32_t d = tbase + 128 * (u & 1);
+                const uint32_t dq = dQ + (u & 1) * 2048;
                 if (elect_one()) {
+#pragma unroll 1
+                    for (int hf = 0; hf < halves; ++hf)
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        if (k < xsteps) umma_bf16(tOx, desc_add(dq, kmajor_step(128, k)), desc_add(dS, k * kMnStep), id_x, k > 0);
-                    umma_commit(&empty_q[u & 1]);
-                    if (r == R - 1) umma_commit(&qs_done);
-                }
-                __syncwarp();
-                // The buffer of the next Q K^T last held P of unit u-1, whose product is done
-                // (o_free above). V's rows past the last token hold zeros (tail_ready).
-                const int cn = r == R - 1 ? c + 1 : c, rn = r == R - 1 ? 0 : r + 1;
-                ok = (cn == nt || issue_qk(cn, rn, u + 1)) && wait_issue_warp(&full_v[c & 1], (c >> 1) & 1, abort_p) &&
-                     wait_issue_warp(&p_ready[u & 1], (u >> 1) & 1, abort_p) &&
-                     (!partial || c < nt - 1 || r > 0 || wait_issue_warp(&tail_ready, 0, abort_p));
-                if (!ok) break;
-                tc_fence_after();
-                const int steps = blocks_of(c) * (kBlock / 16);
-                const uint32_t tP = tbase + 128 * (u & 1);
-                const uint64_t dv = desc_add(dV, (c & 1) * 16384);
-                if (elect_one()) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        if (k < steps) umma_bf16_ts(tOi, tP + 32 * (k >> 1) + 8 * (k & 1), desc_add(dv, k * kMnStep), id_v, k > 0);
-                    umma_commit(&o_done);
-                    if (r == R - 1) umma_commit(&empty_v[c & 1]);
+                        for (int k = 0; k < 4; ++k)
+                            umma(d, dq + hf * 1024 + 2 * k, dk + hf * 1024 + 2 * k, id, hf + k > 0);
+                    umma_commit(&bars[QK_DONE + (u & 1)]);
+                    umma_commit(&bars[EMPTY_Q + (u & 1)]);
+                    if (r == R - 1) umma_commit(&bars[EMPTY_K + (c & 1)]);
                 }
                 __syncwarp();
             }
         }
         // Every MMA issued above has completed once this commit arrives.
-        if (elect_one()) umma_commit(&drained[0]);
+        if (elect_one()) umma_commit(&bars[DRAINED + 0]);
         __syncwarp();
-        mbar_wait(&drained[0], 0);
+        mbar_wait(&bars[DRAINED + 0], 0);
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ UMMA issuer: Oi, Ox
+        const uint32_t id_x = idesc_bf16(128, 128, 0, 1), id_v = idesc_bf16(128, 64, 0, 1);
+        const uint32_t dQ = desc_lo(smem_u32(sm + kOutQ));
+        const uint32_t dV = desc_lo(smem_u32(sm + kOutV)), dS = desc_lo(smem_u32(sm + kOutS));
+        // test hook (stall): a wait that runs out
+        if (a.stall && nt > 0) wait_bar(&bars[STALL], 0, abort_p);
+        bool ok = true;
+        int u = 0;
+#pragma unroll 1
+        for (int c = 0; c < nt && ok; ++c) {
+            const bool st = c > 0 || has_init;
+            const int xhalves = st ? halves : 0, nb = blocks_of(c);
+            const uint32_t dv = dV + (c & 1) * 1024;
+#pragma unroll 1
+            for (int r = 0; r < R; ++r, ++u) {
+                if (r == 0 && st) wait_bar(&bars[S_READY], has_init ? c : c - 1, abort_p);
+                wait_bar(&bars[FULL_Q + (u & 1)], u >> 1, abort_p);
+                if (u > 0) wait_bar(&bars[O_FREE], u - 1, abort_p);
+                if (!(ok = go_on(abort_p))) break;
+                tc_fence_after();
+                const uint32_t dq = dQ + (u & 1) * 2048;
+                if (elect_one()) {
+#pragma unroll 1
+                    for (int hf = 0; hf < xhalves; ++hf)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            umma(tOx, dq + hf * 1024 + 2 * k, dS + (hf * 4 + k) * 128, id_x, hf + k > 0);
+                    umma_commit(&bars[EMPTY_Q + (u & 1)]);
+                    if (r == R - 1) umma_commit(&bars[QS_DONE]);
+                }
+                __syncwarp();
+                // V's rows past the last token hold zeros (tail_ready).
+                if (r == 0) wait_bar(&bars[FULL_V + (c & 1)], c >> 1, abort_p);
+                if (r == 0 && partial && c == nt - 1) wait_bar(&bars[TAIL_READY], 0, abort_p);
+                wait_bar(&bars[P_READY + (u & 1)], u >> 1, abort_p);
+                if (!(ok = go_on(abort_p))) break;
+                tc_fence_after();
+                const uint32_t tP = tbase + 128 * (u & 1);
+                if (elect_one()) {
+#pragma unroll 1
+                    for (int n = 0; n < nb; ++n)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) umma_ts(tOi, tP + 32 * n + 8 * k, dv + (2 * n + k) * 128, id_v, n + k > 0);
+                    umma_commit(&bars[O_DONE + (u & 1)]);
+                    if (r == R - 1) umma_commit(&bars[EMPTY_V + (c & 1)]);
+                }
+                __syncwarp();
+            }
+        }
+        if (elect_one()) umma_commit(&bars[DRAINED + 1]);
+        __syncwarp();
+        mbar_wait(&bars[DRAINED + 1], 0);
     } else if (warp == 2) {
-        // ------------------------------------------------------------ UMMA issuer: the state
-        regs_dec<56>();
+        // ------------------------------------------------------------ UMMA issuer: D
         // D = K^T (w V), for every chunk that another one follows (all of them full).
         const uint32_t id = idesc_bf16(128, 64, 1, 1);
-        const uint64_t dK = smem_desc(smem_u32(sm), 16384, 1024), dW = smem_desc(smem_u32(sm + kOutW), 16384, 1024);
+        const uint32_t dK = desc_lo(smem_u32(sm)), dW = desc_lo(smem_u32(sm + kOutW));
 #pragma unroll 1
         for (int c = 0; c + 1 < nt; ++c) {
-            // w_ready also says that the last D has been read
-            if (!wait_issue_warp(&full_k[c & 1], (c >> 1) & 1, abort_p) || !wait_issue_warp(&w_ready, c & 1, abort_p)) break;
+            wait_bar(&bars[FULL_K + (c & 1)], c >> 1, abort_p);
+            wait_bar(&bars[W_READY], c, abort_p);
+            if (c > 0) wait_bar(&bars[D_FREE], c - 1, abort_p);
+            if (!go_on(abort_p)) break;
             tc_fence_after();
-            const uint64_t dk = desc_add(dK, (c & 1) * 32768);
+            const uint32_t dk = dK + (c & 1) * 2048;
             if (elect_one()) {
+#pragma unroll 1
+                for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int k = 0; k < 8; ++k) umma_bf16(tD, desc_add(dk, k * kMnStep), desc_add(dW, k * kMnStep), id, k > 0);
-                umma_commit(&d_done);
-                umma_commit(&empty_k[c & 1]);
-                umma_commit(&empty_v[c & 1]);
+                    for (int k = 0; k < 4; ++k) umma(tD, dk + (4 * n + k) * 128, dW + (4 * n + k) * 128, id, n + k > 0);
+                umma_commit(&bars[D_DONE]);
+                umma_commit(&bars[EMPTY_K + (c & 1)]);
+                umma_commit(&bars[EMPTY_V + (c & 1)]);
             }
             __syncwarp();
         }
-        if (elect_one()) umma_commit(&drained[1]);
+        if (elect_one()) umma_commit(&bars[DRAINED + 2]);
         __syncwarp();
-        mbar_wait(&drained[1], 0);
-    } else if (warp < 4) {
-        regs_dec<56>();
-        // nothing: the groups below start at a multiple of four warps (TMEM lane quarters)
+        mbar_wait(&bars[DRAINED + 2], 0);
     } else if (warp < 4 + kScoreWarps) {
-        // ------------------------------------------------------------ scores
+        // ------------------------------------------------------------ scores and w V
         // Thread: token row t = 32 quarter + lane; of the four 32-wide column blocks, 0 and 3
         // (half 0) or 1 and 2 (half 1), so that every warp has about the same share of the
-        // causal triangle.
+        // causal triangle. As a writer of w V: token rows wt + 32 i, 8 columns.
         const int quarter = warp & 3, half = (warp - 4) >> 2, t = 32 * quarter + lane;
         const uint32_t lanes = (uint32_t)quarter << 21;
-        int u = 0;
+        const int wt = (tid - 128) >> 3, wc = tid & 7;
+        auto write_w = [&](int c) {          // w V of a full chunk
+            wait_bar(&bars[FULL_V + (c & 1)], c >> 1, abort_p);
+            if (c > 0) wait_bar(&bars[D_DONE], c - 1, abort_p);            // its buffer has been read
+            const uint32_t sv = smem_u32(sm + kOutV) + (c & 1) * 16384, sw = smem_u32(sm + kOutW);
+#pragma unroll 2
+            for (int i = 0; i < 4; ++i) {
+                const int s = wt + 32 * i;
+                const float w = pw[kTcC - 1 - s];
+                const uint4 x = ld_shared_v4(tile_at(sv, s, wc));
+                const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+                uint32_t y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = pack_bf16(fmul2(bf16x2_to_f2(xs[e]), make_float2(w, w)));
+                st_shared_v4(tile_at(sw, s, wc), y[0], y[1], y[2], y[3]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[W_READY]);
+        };
+        int u = 0, w_next = 0;               // unit; chunk whose w V is written next
 #pragma unroll 1
         for (int c = 0; c < nt; ++c) {
             const int nb = blocks_of(c);
+            if (partial && c == nt - 1) {
+                // Rows past the sequence's end (another sequence's, or nothing) are zeroed in V,
+                // since a score of 0 times what they hold need not be 0.
+                wait_bar(&bars[FULL_V + (c & 1)], c >> 1, abort_p);
+                for (int s = len_of(c) + wt; s < kBlock * nb; s += 32)
+                    st_shared_v4(tile_at(smem_u32(sm + kOutV) + (c & 1) * 16384, s, wc), 0, 0, 0, 0);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[TAIL_READY]);
+            }
 #pragma unroll 1
             for (int r = 0; r < R; ++r, ++u) {
                 const uint32_t tP = tbase + 128 * (u & 1) + lanes;
-                wait_abort(&qk_done[u & 1], (u >> 1) & 1, abort_p);
+                wait_bar(&bars[QK_DONE + (u & 1)], u >> 1, abort_p);
                 tc_fence_after();
 #pragma unroll 1
                 for (int e = 0; e < 2; ++e) {
@@ -564,28 +584,14 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
                         uint32_t x[32];
                         tmem_ld32(tP + 32 * b, x);
                         tmem_wait_ld();
-                        if (b < quarter) {
-                            // lam^(t-s) = lam^(t - 32b - 31) lam^(31 - j): both exponents >= 0
-                            const float rf = pw[t - 32 * b - 31];
-                            const float2 rf2 = make_float2(rf, rf);
+                        // lam^(t-s); s > t is dropped whatever the score holds
+                        const int d = t - 32 * b;
+                        const float* f = pw + d;
 #pragma unroll
-                            for (int i = 0; i < 32; i += 4) {
-                                const float4 f = *reinterpret_cast<const float4*>(rev + i);
-                                const float2 lo = fmul2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
-                                                        fmul2(rf2, make_float2(f.x, f.y)));
-                                const float2 hi = fmul2(make_float2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])),
-                                                        fmul2(rf2, make_float2(f.z, f.w)));
-                                p[i / 2] = pack_bf16(lo);
-                                p[i / 2 + 1] = pack_bf16(hi);
-                            }
-                        } else {
-                            // diagonal block: s > t is dropped whatever the score holds
-#pragma unroll
-                            for (int i = 0; i < 32; i += 2) {
-                                const float y0 = i <= lane ? __uint_as_float(x[i]) * pw[lane - i] : 0.f;
-                                const float y1 = i + 1 <= lane ? __uint_as_float(x[i + 1]) * pw[lane - i - 1] : 0.f;
-                                p[i / 2] = pack_bf16(y0, y1);
-                            }
+                        for (int i = 0; i < 32; i += 2) {
+                            const float y0 = i <= d ? __uint_as_float(x[i]) * f[-i] : 0.f;
+                            const float y1 = i + 1 <= d ? __uint_as_float(x[i + 1]) * f[-i - 1] : 0.f;
+                            p[i / 2] = pack_bf16(y0, y1);
                         }
                     }
                     tmem_st16(tP + 32 * b, p);
@@ -593,7 +599,11 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_ready[u & 1]);
+                if (lane == 0) mbar_arrive(&bars[P_READY + (u & 1)]);
+                // w V of the first chunk, and of the next one once the last unit's scores are on
+                // their way (its V may be loaded behind the Q of this chunk's units).
+                const int upto = min(nt - 2, r == R - 1 ? c + 1 : c);
+                while (w_next <= upto) write_w(w_next++);
             }
         }
     } else if (warp < 4 + kScoreWarps + kOutWarps) {
@@ -611,7 +621,7 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
                                ((sg.start + (int64_t)c * kTcC + t) * a.H + g * R) * (int64_t)a.V + v0 + 32 * half;
 #pragma unroll 1
             for (int r = 0; r < R; ++r, ++u, p += a.V) {
-                wait_abort(&o_done, u & 1, abort_p);
+                wait_bar(&bars[O_DONE + (u & 1)], u >> 1, abort_p);
                 tc_fence_after();
 #pragma unroll 1
                 for (int e = 0; e < 2; ++e) {
@@ -625,7 +635,7 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
                     if (e == 1) {
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&o_free);
+                        if (lane == 0) mbar_arrive(&bars[O_FREE]);
                     }
 #pragma unroll
                     for (int i = 0; i < 16; i += 2) {
@@ -645,98 +655,90 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
             }
         }
     } else {
-        // ------------------------------------------------------------ w V and the state
-        regs_inc<80>();
-        // Thread: state row k = 32 quarter + lane, 32 of the 64 V columns; as a writer of w V:
-        // token rows wt + 32 i, 8 columns.
+        // ------------------------------------------------------------ the state
+        // Thread: state row k = 32 quarter + lane, 32 of the 64 V columns.
         const int quarter = warp & 3, half = (warp - 4 - kScoreWarps - kOutWarps) >> 2, k = 32 * quarter + lane;
-        const int wi = tid - 32 * (4 + kScoreWarps + kOutWarps), wt = wi >> 3, wc = wi & 7;
-        float S[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) S[i] = 0.f;
-        {
-            // The state entering the segment, and the final state after the last one.
-            const Column col(k, 32 * half, nv, K);
+        // The state entering the segment, and the final state after the last one: a warp takes
+        // columns of V one by one, lanes side by side along K, eight elements a lane in flight;
+        // then through shared memory (the place of the operand S; rows of 64 floats, 16-byte
+        // chunks exchanged to spread the banks) to the threads that keep them.
+        const uint32_t sS = smem_u32(sm + kOutS);
+        if (has_init || fp >= 0) {
             const float* slots = a.slots + (int64_t)sg.slot0 * per_state + head;
-            if (ip >= 0) take<true>(S, col, a.two_pass ? slots : a.init + ip * per_state + head, make_float2(0.f, 0.f));
+            const float* first = a.two_pass ? slots : a.init + ip * per_state + head;
+            float* fin = a.fin + fp * per_state + head;
+            const int w8 = warp - (4 + kScoreWarps + kOutWarps);
 #pragma unroll 1
-            for (int j = 1; j <= sg.j; ++j) take<false>(S, col, slots + j * per_state, lam_seg);
-            if (fp >= 0) {
-                const float* add = slots + (int64_t)(sg.j + 1) * per_state + col.offset;
-                float* to = a.fin + fp * per_state + head + col.offset;
+            for (int step = 0; step < 4; ++step) {
+                float x[8];
+                int at[8];
 #pragma unroll
-                for (int i = 0; i < 32; ++i, add += K, to += K)
-                    if (i < col.rows) *to = fmaf(lam_len.x, S[i], fmaf(lam_len.y, S[i], *add));
+                for (int i = 0; i < 8; ++i) {
+                    const int v = w8 + 8 * (2 * step + (i >> 2)), kk = lane + 32 * (i & 3);
+                    at[i] = v < nv && kk < K ? v * K + kk : -1;
+                    x[i] = ip >= 0 && at[i] >= 0 ? first[at[i]] : 0.f;
+                }
+#pragma unroll 1
+                for (int j = 1; j <= sg.j; ++j)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (at[i] >= 0) x[i] = fmaf(lam_seg.x, x[i], fmaf(lam_seg.y, x[i], slots[j * per_state + at[i]]));
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int v = w8 + 8 * (2 * step + (i >> 2)), kk = lane + 32 * (i & 3);
+                    const uint32_t to = sS + kk * 256 + ((((uint32_t)v >> 2) ^ (kk & 15)) << 4) + (v & 3) * 4;
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(to), "f"(x[i]) : "memory");
+                    if (fp >= 0 && at[i] >= 0)
+                        fin[at[i]] = fmaf(lam_len.x, x[i], fmaf(lam_len.y, x[i], slots[(sg.j + 1) * per_state + at[i]]));
+                }
             }
+            named_barrier(1, 32 * kStateWarps);
         }
-        auto write_w = [&](int c) {          // w V of a full chunk
-            wait_abort(&full_v[c & 1], (c >> 1) & 1, abort_p);
-            const uint32_t sv = smem_u32(sm + kOutV) + (c & 1) * 16384, sw = smem_u32(sm + kOutW);
-#pragma unroll 2
-            for (int i = 0; i < 4; ++i) {
-                const int s = wt + 32 * i;
-                const float w = pw[kTcC - 1 - s];
-                const uint4 x = ld_shared_v4(tile_at(sv, s, wc));
-                const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-                uint32_t y[4];
+        float2 S[16];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = pack_bf16(fmul2(bf16x2_to_f2(xs[e]), make_float2(w, w)));
-                st_shared_v4(tile_at(sw, s, wc), y[0], y[1], y[2], y[3]);
+        for (int i = 0; i < 8; ++i) {
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (has_init) x = ld_shared_v4(sS + k * 256 + (((8 * half + i) ^ (k & 15)) << 4));
+            S[2 * i] = make_float2(__uint_as_float(x.x), __uint_as_float(x.y));
+            S[2 * i + 1] = make_float2(__uint_as_float(x.z), __uint_as_float(x.w));
+        }
+        if (has_init) named_barrier(1, 32 * kStateWarps);        // read before the operand takes the place
+        const float2 lam = make_float2(lam_full.x, lam_full.x);
+#pragma unroll 1
+        for (int c = has_init ? -1 : 0; c + 1 < nt; ++c) {        // S entering chunk c + 1
+            if (c >= 0) {
+                wait_bar(&bars[D_DONE], c, abort_p);
+                tc_fence_after();
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    uint32_t d[8];
+                    tmem_ld8(tD + ((uint32_t)quarter << 21) + 32 * half + 8 * e, d);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        S[4 * e + i] =
+                            ffma2(lam, S[4 * e + i], make_float2(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1])));
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[D_FREE]);
+                wait_bar(&bars[QS_DONE], c, abort_p);
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&w_ready);
-        };
-        auto hand_over = [&]() {             // S as the B operand of Q S: row k, a bf16 pair
-            const uint32_t base = smem_u32(sm + kOutS);
+            // S as the B operand of Q S: row k, a bf16 pair
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 uint32_t h[4], l[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float2 x = make_float2(S[8 * i + 2 * e], S[8 * i + 2 * e + 1]);
-                    h[e] = pack_bf16(x);
-                    l[e] = pack_bf16(fsub2(x, bf16x2_to_f2(h[e])));
+                    h[e] = pack_bf16(S[4 * i + e]);
+                    l[e] = pack_bf16(fsub2(S[4 * i + e], bf16x2_to_f2(h[e])));
                 }
-                st_shared_v4(tile_at(base, k, 4 * half + i), h[0], h[1], h[2], h[3]);
-                st_shared_v4(tile_at(base + 16384, k, 4 * half + i), l[0], l[1], l[2], l[3]);
+                st_shared_v4(tile_at(sS, k, 4 * half + i), h[0], h[1], h[2], h[3]);
+                st_shared_v4(tile_at(sS + 16384, k, 4 * half + i), l[0], l[1], l[2], l[3]);
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&s_ready);
-        };
-        if (has_init && nt > 0) hand_over();
-        if (nt > 1) write_w(0);
-#pragma unroll 1
-        for (int c = 0; c + 1 < nt; ++c) {
-            wait_abort(&d_done, c & 1, abort_p);
-            tc_fence_after();
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                uint32_t d[16];
-                tmem_ld16(tD + ((uint32_t)quarter << 21) + 32 * half + 16 * e, d);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float& s = S[16 * e + i];
-                    s = fmaf(lam_full.x, s, fmaf(lam_full.y, s, __uint_as_float(d[i])));
-                }
-            }
-            tc_fence_before();
-            wait_abort(&qs_done, c & 1, abort_p);
-            hand_over();
-            if (c + 2 < nt) write_w(c + 1);
-        }
-        if (partial) {
-            // Rows past the sequence's end (another sequence's, or nothing) are zeroed in V,
-            // since a score of 0 times what they hold need not be 0.
-            const int c = nt - 1, len = len_of(c), rows = kBlock * blocks_of(c);
-            wait_abort(&full_v[c & 1], (c >> 1) & 1, abort_p);
-            for (int s = len + wt; s < rows; s += 32)
-                st_shared_v4(tile_at(smem_u32(sm + kOutV) + (c & 1) * 16384, s, wc), 0, 0, 0, 0);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&tail_ready);
+            if (lane == 0) mbar_arrive(&bars[S_READY]);
         }
     }
     tc_fence_before();

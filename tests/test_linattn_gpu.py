@@ -101,6 +101,23 @@ def test_dense_prompts(ssd, cuda_dev, b, L, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("H,Hk,K,V", [(8, 1, 128, 64), (6, 2, 64, 128), (2, 2, 128, 128)])
+def test_many_chunks(ssd, cuda_dev, H, Hk, K, V, dtype):
+    """Ten chunks in one segment and in several, with and without a partial one at the end."""
+    lens = [1280, 1217]
+    d = make(cuda_dev, lens, dtype, H, Hk, K, V, seed=H)
+    ref = LO.linattn(d["q"], d["k"], d["v"], d["ld"], K ** -0.5, d["s0"], lens)
+    for seg in (1 << 20, 384):
+        ssd.set_segment_tokens(seg)
+        try:
+            o, fin = ssd.linear_attn_fwd(d["q"], d["k"], d["v"], d["ld"], init_state=d["s0"], cu_seqlens=cu_of(lens, cuda_dev))
+        finally:
+            ssd.set_segment_tokens(0)
+        ssd.device_status()
+        check(o, fin, ref, dtype, K, 1280)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_long_prompt_keeps_the_precision_of_slow_decays(ssd, cuda_dev, dtype):
     """32,768 tokens of one head pair: the state remembers thousands of chunks."""
     L, H, K, V = 32768, 2, 64, 64
