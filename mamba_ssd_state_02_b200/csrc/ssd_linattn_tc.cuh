@@ -10,8 +10,8 @@
 //   output pass: starts from the states of the segments before it, and per chunk
 //       P  = (Q K^T) o lam^(t-s), s <= t        UMMA -> TMEM, warps scale and mask, bf16 -> TMEM
 //       Oi = P V                                UMMA, A from TMEM
-//       Ox = Q [S_hi | S_lo]                    UMMA, N = 128; S = S_hi + S_lo, a bf16 pair
-//       o  = scale (Oi + lam^(t+1) (Ox_hi + Ox_lo))
+//       Ox = Q S_hi + Q S_lo                    UMMA; S = S_hi + S_lo, a bf16 pair
+//       o  = scale (Oi + lam^(t+1) Ox)          (scale is in P)
 //       S' = lam^128 S + K^T (w V)              UMMA, w V rounded to bf16; FP32 in registers
 //     The CTA of a sequence's last segment also writes the final state, from the states of the
 //     state pass alone.
@@ -41,19 +41,18 @@ constexpr int kStateWarps = 8;
 // Bounded waits, as wait_abort and wait_issue of the scan's passes (an expired wait latches
 // SSD_ERR_TIMEOUT and raises the CTA's abort flag, after which every wait returns; the issuing
 // warps look at the flag after their waits and stop), but short: the passes have two dozen
-// waits in loops that ten warps with code of their own run at once, and their code has to
-// stay within the instruction cache (at twice the size the output pass took 1.25 times as
-// long). The budget is 4e9 cycles of the 32-bit clock.
+// waits in loops that ten kinds of warps run at once, and once their code outgrows the
+// instruction cache every one of them runs at the speed of its misses (at 107 KB of code the
+// output pass took 1.3 times as long as at 40 KB). A try that fails blocks for about 4 us
+// (measured), so the tries add up to about 2 s.
+constexpr uint32_t kWaitTries = 1u << 19;
+
 __device__ __forceinline__ void wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-    if (tc::mbar_try_wait_sleep(bar, parity & 1)) return;
-    const uint32_t t0 = (uint32_t)clock();
-    while (!tc::mbar_try_wait_sleep(bar, parity & 1)) {
-        if (*abort_flag) return;
-        if ((uint32_t)clock() - t0 > 4000000000u) {
+    for (uint32_t n = 0; !tc::mbar_try_wait_sleep(bar, parity & 1) && !*abort_flag; ++n)
+        if (n == kWaitTries) {
             latch_error(SSD_ERR_TIMEOUT);
             *abort_flag = 1;
         }
-    }
 }
 
 // For an issuing warp, after its waits: none of them was given up.
@@ -285,8 +284,8 @@ k_la_tc_state(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
 //
 // Shared memory: K, V, Q (two buffers each), S (a bf16 pair), w V. TMEM columns: Q K^T [0, 128)
 // and [128, 256) (units alternate), P of a 32-token block in the first 16 columns of the
-// block's scores (read and written by the same thread), Oi [256, 320), Ox [320, 448), D
-// [448, 512).
+// block's scores (read and written by the same thread), Oi [256, 320), Ox [320, 384), D
+// [384, 448).
 
 // A matrix descriptor's low word: start address, and the distance between 64-wide blocks of an
 // MN-major operand (16 KB; not read for K-major ones). The high word is the same for all. In
@@ -324,7 +323,9 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
 
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ float pw_pad[32 + kTcC + 1];  // 32 zeros, then lam^0 .. lam^128
+    __shared__ float pw[kTcC + 1];           // lam^0 .. lam^128
+    __shared__ float pws[32 + kTcC];         // 32 zeros, then scale lam^0 .. lam^127
+    __shared__ __align__(16) float rev[32];  // lam^31 .. lam^0
     __shared__ float2 lam_full, lam_seg, lam_len;
     // pairs for the two buffers of K, V, Q and the scores, then single barriers
     enum { FULL_K = 0, EMPTY_K = 2, FULL_V = 4, EMPTY_V = 6, FULL_Q = 8, EMPTY_Q = 10, QK_DONE = 12, P_READY = 14, O_DONE = 16,
@@ -332,11 +333,18 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
     __shared__ uint64_t bars[BARS];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
-    const float* pw = pw_pad + 32;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const float gd = a.log_decay[g];
-    if (tid < 32 + kTcC + 1) pw_pad[tid] = tid < 32 ? 0.f : (float)pow_decay(gd, tid - 32);
+    if (tid <= kTcC) {
+        const float x = (float)pow_decay(gd, tid);
+        pw[tid] = x;
+        if (tid < kTcC) pws[32 + tid] = a.scale * x;
+        if (tid < 32) {
+            pws[tid] = 0.f;
+            rev[31 - tid] = x;
+        }
+    }
     if (tid == 256) lam_full = pow2f(gd, kTcC);
     if (tid == 288) lam_seg = pow2f(gd, a.Ls);
     if (tid == 320) lam_len = pow2f(gd, sg.len);
@@ -368,7 +376,7 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tbase = tmem_slot, tOi = tbase + 256, tOx = tbase + 320, tD = tbase + 448;
+    const uint32_t tbase = tmem_slot, tOi = tbase + 256, tOx = tbase + 320, tD = tbase + 384;
     volatile int* abort_p = &abort_flag;
     const bool has_init = ip >= 0 || sg.j > 0;                    // the first chunk meets a state
 
@@ -449,7 +457,7 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
         mbar_wait(&bars[DRAINED + 0], 0);
     } else if (warp == 1) {
         // ------------------------------------------------------------ UMMA issuer: Oi, Ox
-        const uint32_t id_x = idesc_bf16(128, 128, 0, 1), id_v = idesc_bf16(128, 64, 0, 1);
+        const uint32_t id_v = idesc_bf16(128, 64, 0, 1);
         const uint32_t dQ = desc_lo(smem_u32(sm + kOutQ));
         const uint32_t dV = desc_lo(smem_u32(sm + kOutV)), dS = desc_lo(smem_u32(sm + kOutS));
         // test hook (stall): a wait that runs out
@@ -473,8 +481,8 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
 #pragma unroll 1
                     for (int hf = 0; hf < xhalves; ++hf)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            umma(tOx, dq + hf * 1024 + 2 * k, dS + (hf * 4 + k) * 128, id_x, hf + k > 0);
+                        for (int k = 0; k < 8; ++k)                // S_hi, then S_lo
+                            umma(tOx, dq + hf * 1024 + 2 * (k & 3), dS + (hf * 4 + (k & 3)) * 128 + (k >> 2) * 1024, id_v, hf + k > 0);
                     umma_commit(&bars[EMPTY_Q + (u & 1)]);
                     if (r == R - 1) umma_commit(&bars[QS_DONE]);
                 }
@@ -535,20 +543,20 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
         const int quarter = warp & 3, half = (warp - 4) >> 2, t = 32 * quarter + lane;
         const uint32_t lanes = (uint32_t)quarter << 21;
         const int wt = (tid - 128) >> 3, wc = tid & 7;
+        const uint32_t w_at = tile_at(smem_u32(sm), wt, wc);     // row wt + 32 i is 4096 i further
         auto write_w = [&](int c) {          // w V of a full chunk
             wait_bar(&bars[FULL_V + (c & 1)], c >> 1, abort_p);
             if (c > 0) wait_bar(&bars[D_DONE], c - 1, abort_p);            // its buffer has been read
-            const uint32_t sv = smem_u32(sm + kOutV) + (c & 1) * 16384, sw = smem_u32(sm + kOutW);
-#pragma unroll 2
+            const uint32_t from = w_at + kOutV + (c & 1) * 16384, to = w_at + kOutW;
+#pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int s = wt + 32 * i;
-                const float w = pw[kTcC - 1 - s];
-                const uint4 x = ld_shared_v4(tile_at(sv, s, wc));
+                const uint4 x = ld_shared_v4(from + i * 4096);
                 const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+                const float w = pw[kTcC - 1 - wt - 32 * i];
                 uint32_t y[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) y[e] = pack_bf16(fmul2(bf16x2_to_f2(xs[e]), make_float2(w, w)));
-                st_shared_v4(tile_at(sw, s, wc), y[0], y[1], y[2], y[3]);
+                st_shared_v4(to + i * 4096, y[0], y[1], y[2], y[3]);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -584,14 +592,27 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
                         uint32_t x[32];
                         tmem_ld32(tP + 32 * b, x);
                         tmem_wait_ld();
-                        // lam^(t-s); s > t is dropped whatever the score holds
-                        const int d = t - 32 * b;
-                        const float* f = pw + d;
+                        if (b < quarter) {
+                            // lam^(t-s) = lam^(t - 32b - 31) lam^(31 - j): both exponents >= 0
+                            const float rf = pws[32 + t - 32 * b - 31];
+                            const float2 rf2 = make_float2(rf, rf);
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            const float y0 = i <= d ? __uint_as_float(x[i]) * f[-i] : 0.f;
-                            const float y1 = i + 1 <= d ? __uint_as_float(x[i + 1]) * f[-i - 1] : 0.f;
-                            p[i / 2] = pack_bf16(y0, y1);
+                            for (int i = 0; i < 32; i += 4) {
+                                const float4 f = *reinterpret_cast<const float4*>(rev + i);
+                                p[i / 2] = pack_bf16(fmul2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
+                                                           fmul2(rf2, make_float2(f.x, f.y))));
+                                p[i / 2 + 1] = pack_bf16(fmul2(make_float2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])),
+                                                               fmul2(rf2, make_float2(f.z, f.w))));
+                            }
+                        } else {
+                            // diagonal block: s > t is dropped whatever the score holds
+                            const float* f = pws + 32 + lane;
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2) {
+                                const float y0 = i <= lane ? __uint_as_float(x[i]) * f[-i] : 0.f;
+                                const float y1 = i + 1 <= lane ? __uint_as_float(x[i + 1]) * f[-i - 1] : 0.f;
+                                p[i / 2] = pack_bf16(y0, y1);
+                            }
                         }
                     }
                     tmem_st16(tP + 32 * b, p);
@@ -611,7 +632,7 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
         // Thread: token row t, 32 of the 64 columns.
         const int quarter = warp & 3, half = (warp - 4 - kScoreWarps) >> 2, t = 32 * quarter + lane;
         const uint32_t lanes = ((uint32_t)quarter << 21) + 32 * half;
-        const float wx = pw[t + 1] * a.scale;
+        const float2 wx = make_float2(pw[t + 1] * a.scale, pw[t + 1] * a.scale);
         int u = 0;
 #pragma unroll 1
         for (int c = 0; c < nt; ++c) {
@@ -625,12 +646,9 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
                 tc_fence_after();
 #pragma unroll 1
                 for (int e = 0; e < 2; ++e) {
-                    uint32_t out[8], x[16], h[16], l[16];
+                    uint32_t out[8], x[16], y[16];
                     tmem_ld16(tOi + lanes + 16 * e, x);
-                    if (st) {
-                        tmem_ld16(tOx + lanes + 16 * e, h);
-                        tmem_ld16(tOx + lanes + 64 + 16 * e, l);
-                    }
+                    if (st) tmem_ld16(tOx + lanes + 16 * e, y);
                     tmem_wait_ld();
                     if (e == 1) {
                         tc_fence_before();
@@ -638,13 +656,10 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
                         if (lane == 0) mbar_arrive(&bars[O_FREE]);
                     }
 #pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
-                        float2 y = make_float2(__uint_as_float(x[i]) * a.scale, __uint_as_float(x[i + 1]) * a.scale);
-                        if (st) {
-                            y.x = fmaf(wx, __uint_as_float(h[i]) + __uint_as_float(l[i]), y.x);
-                            y.y = fmaf(wx, __uint_as_float(h[i + 1]) + __uint_as_float(l[i + 1]), y.y);
-                        }
-                        out[i / 2] = pack_bf16(y);
+                    for (int i = 0; i < 8; ++i) {
+                        float2 z = make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+                        if (st) z = ffma2(wx, make_float2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])), z);
+                        out[i] = pack_bf16(z);
                     }
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
