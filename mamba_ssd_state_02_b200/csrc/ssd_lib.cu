@@ -1456,19 +1456,20 @@ ssd_status launch_la(const LaPlan& p, int64_t segs, cudaStream_t st) {
         la::k_la_simt<OUT><<<grid, la::kSimtThreads, smem, st>>>(a);
         return SSD_OK;
     }
-    CUtensorMap mq{}, mk{}, mv{};
+    CUtensorMap mq{}, mk{}, mv{}, mo{};
     const uint64_t T = (uint64_t)p.T;
     if (T > 0 && ((OUT && !make_map3(&mq, a.q, a.K, a.H, T, (uint64_t)a.K * 2, (uint64_t)a.q_stride * 2, 64, 1, la::kTcC)) ||
+                  (OUT && !make_map3(&mo, a.o, a.V, a.H, T, (uint64_t)a.V * 2, (uint64_t)a.H * a.V * 2, 64, 1, la::kTcC)) ||
                   !make_map3(&mk, a.k, a.K, a.Hk, T, (uint64_t)a.K * 2, (uint64_t)a.k_stride * 2, 64, 1, la::kTcC) ||
                   !make_map3(&mv, a.v, a.V, a.Hk, T, (uint64_t)a.V * 2, (uint64_t)a.v_stride * 2, 64, 1, la::kTcC)))
-        return fail(SSD_ERR_CUDA, "cuTensorMapEncodeTiled failed (q/k/v tensor maps)");
+        return fail(SSD_ERR_CUDA, "cuTensorMapEncodeTiled failed (q/k/v/o tensor maps)");
     la::Args b = a;
     b.stall = g_test_stall.load() == (OUT ? 2 : 1);
     if (OUT) {
         cudaError_t e = cudaFuncSetAttribute(la::k_la_tc_out, cudaFuncAttributeMaxDynamicSharedMemorySize, la::kOutSmem);
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(linear attention)");
         StageScope sc(ST_LA_SCAN, st);
-        la::k_la_tc_out<<<grid, la::kOutThreads, la::kOutSmem, st>>>(mq, mk, mv, b);
+        la::k_la_tc_out<<<grid, la::kOutThreads, la::kOutSmem, st>>>(mq, mk, mv, mo, b);
     } else {
         cudaError_t e = cudaFuncSetAttribute(la::k_la_tc_state, cudaFuncAttributeMaxDynamicSharedMemorySize, la::kStateSmem);
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(linear attention)");

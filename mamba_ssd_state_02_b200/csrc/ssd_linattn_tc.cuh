@@ -10,8 +10,8 @@
 //   output pass: starts from the states of the segments before it, and per chunk
 //       P  = (Q K^T) o lam^(t-s), s <= t        UMMA -> TMEM, warps scale and mask, bf16 -> TMEM
 //       Oi = P V                                UMMA, A from TMEM
-//       Ox = Q S_hi + Q S_lo                    UMMA; S = S_hi + S_lo, a bf16 pair
-//       o  = scale (Oi + lam^(t+1) Ox)          (scale is in P)
+//       Ox = Q [S_hi | S_lo]                    UMMA, N = 128; S = S_hi + S_lo, a bf16 pair
+//       o  = Oi + scale lam^(t+1) (Ox_hi + Ox_lo)       (P carries scale)
 //       S' = lam^128 S + K^T (w V)              UMMA, w V rounded to bf16; FP32 in registers
 //     The CTA of a sequence's last segment also writes the final state, from the states of the
 //     state pass alone.
@@ -57,6 +57,15 @@ __device__ __forceinline__ void wait_bar(uint64_t* bar, uint32_t parity, volatil
 
 // For an issuing warp, after its waits: none of them was given up.
 __device__ __forceinline__ bool go_on(volatile int* abort_flag) { return __all_sync(0xffffffffu, *abort_flag == 0); }
+
+__device__ __forceinline__ float2 fadd2(float2 x, float2 y) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+    return d;
+}
 
 // Row `r` (0..127), 16-byte chunk `c` of a [128][64] bf16 tile in the 128-byte swizzle.
 __device__ __forceinline__ uint32_t tile_at(uint32_t base, int r, int c) { return base + tc::swz(r, c); }
@@ -282,10 +291,12 @@ k_la_tc_state(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
 // into L2. Q K^T runs one unit ahead, in the gap that the outputs leave in the tensor pipe
 // while they are read.
 //
-// Shared memory: K, V, Q (two buffers each), S (a bf16 pair), w V. TMEM columns: Q K^T [0, 128)
+// Shared memory: K, V, Q (two buffers each), S (a bf16 pair), w V, and a tile of o on its way
+// out by TMA (a thread's row of o is 64 bytes in another line than its neighbours'; stored from
+// registers it took a seventh of the pass). TMEM columns: Q K^T [0, 128)
 // and [128, 256) (units alternate), P of a 32-token block in the first 16 columns of the
-// block's scores (read and written by the same thread), Oi [256, 320), Ox [320, 384), D
-// [384, 448).
+// block's scores (read and written by the same thread), Oi [256, 320), Ox [320, 448), D
+// [448, 512).
 
 // A matrix descriptor's low word: start address, and the distance between 64-wide blocks of an
 // MN-major operand (16 KB; not read for K-major ones). The high word is the same for all. In
@@ -304,12 +315,13 @@ __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_
 
 constexpr int kScoreWarps = 8, kOutWarps = 8;
 constexpr int kOutThreads = 32 * (4 + kScoreWarps + kOutWarps + kStateWarps);
-constexpr int kOutV = 65536, kOutQ = 98304, kOutS = 163840, kOutW = 196608;      // K at 0
-constexpr int kOutSmem = 212992 + 1024;
+constexpr int kOutV = 65536, kOutQ = 98304, kOutS = 163840, kOutW = 196608, kOutO = 212992;   // K at 0
+constexpr int kOutSmem = 229376 + 1024;
 
 __global__ void __launch_bounds__(kOutThreads, 1)
 k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-            const __grid_constant__ CUtensorMap map_v, const __grid_constant__ Args a) {
+            const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_o,
+            const __grid_constant__ Args a) {
     using namespace tc;
     const int nvb = (a.V + kTcV - 1) / kTcV;
     const int vb = blockIdx.x % nvb, g = (blockIdx.x / nvb) % a.Hk;
@@ -376,7 +388,7 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tbase = tmem_slot, tOi = tbase + 256, tOx = tbase + 320, tD = tbase + 384;
+    const uint32_t tbase = tmem_slot, tOi = tbase + 256, tOx = tbase + 320, tD = tbase + 448;
     volatile int* abort_p = &abort_flag;
     const bool has_init = ip >= 0 || sg.j > 0;                    // the first chunk meets a state
 
@@ -457,7 +469,7 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
         mbar_wait(&bars[DRAINED + 0], 0);
     } else if (warp == 1) {
         // ------------------------------------------------------------ UMMA issuer: Oi, Ox
-        const uint32_t id_v = idesc_bf16(128, 64, 0, 1);
+        const uint32_t id_x = idesc_bf16(128, 128, 0, 1), id_v = idesc_bf16(128, 64, 0, 1);
         const uint32_t dQ = desc_lo(smem_u32(sm + kOutQ));
         const uint32_t dV = desc_lo(smem_u32(sm + kOutV)), dS = desc_lo(smem_u32(sm + kOutS));
         // test hook (stall): a wait that runs out
@@ -481,8 +493,8 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
 #pragma unroll 1
                     for (int hf = 0; hf < xhalves; ++hf)
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)                // S_hi, then S_lo
-                            umma(tOx, dq + hf * 1024 + 2 * (k & 3), dS + (hf * 4 + (k & 3)) * 128 + (k >> 2) * 1024, id_v, hf + k > 0);
+                        for (int k = 0; k < 4; ++k)
+                            umma(tOx, dq + hf * 1024 + 2 * k, dS + (hf * 4 + k) * 128, id_x, hf + k > 0);
                     umma_commit(&bars[EMPTY_Q + (u & 1)]);
                     if (r == R - 1) umma_commit(&bars[QS_DONE]);
                 }
@@ -631,24 +643,26 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
         // ------------------------------------------------------------ outputs
         // Thread: token row t, 32 of the 64 columns.
         const int quarter = warp & 3, half = (warp - 4 - kScoreWarps) >> 2, t = 32 * quarter + lane;
-        const uint32_t lanes = ((uint32_t)quarter << 21) + 32 * half;
+        const uint32_t lanes = ((uint32_t)quarter << 21) + 32 * half, sO = smem_u32(sm + kOutO);
         const float2 wx = make_float2(pw[t + 1] * a.scale, pw[t + 1] * a.scale);
+        const bool issuer = warp == 4 + kScoreWarps && lane == 0;
         int u = 0;
 #pragma unroll 1
         for (int c = 0; c < nt; ++c) {
-            const bool st = c > 0 || has_init;
-            const int cols = t < len_of(c) ? nv - 32 * half : 0;
-            __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.o) +
-                               ((sg.start + (int64_t)c * kTcC + t) * a.H + g * R) * (int64_t)a.V + v0 + 32 * half;
+            const bool st = c > 0 || has_init, whole = len_of(c) == kTcC;
 #pragma unroll 1
-            for (int r = 0; r < R; ++r, ++u, p += a.V) {
+            for (int r = 0; r < R; ++r, ++u) {
                 wait_bar(&bars[O_DONE + (u & 1)], u >> 1, abort_p);
                 tc_fence_after();
-#pragma unroll 1
+                uint32_t out[16];
+#pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    uint32_t out[8], x[16], y[16];
+                    uint32_t x[16], h[16], l[16];
                     tmem_ld16(tOi + lanes + 16 * e, x);
-                    if (st) tmem_ld16(tOx + lanes + 16 * e, y);
+                    if (st) {
+                        tmem_ld16(tOx + lanes + 16 * e, h);
+                        tmem_ld16(tOx + lanes + 64 + 16 * e, l);
+                    }
                     tmem_wait_ld();
                     if (e == 1) {
                         tc_fence_before();
@@ -658,17 +672,36 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         float2 z = make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
-                        if (st) z = ffma2(wx, make_float2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])), z);
-                        out[i] = pack_bf16(z);
+                        if (st)
+                            z = ffma2(wx, fadd2(make_float2(__uint_as_float(h[2 * i]), __uint_as_float(h[2 * i + 1])),
+                                                make_float2(__uint_as_float(l[2 * i]), __uint_as_float(l[2 * i + 1]))), z);
+                        out[8 * e + i] = pack_bf16(z);
                     }
+                }
+                if (whole) {
+                    if (issuer) bulk_wait_read_all();             // the last tile has left
+                    named_barrier(2, 32 * kOutWarps);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        if (16 * e + 8 * i < cols)
-                            reinterpret_cast<uint4*>(p)[2 * e + i] =
-                                make_uint4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]);
+                    for (int i = 0; i < 4; ++i)
+                        st_shared_v4(tile_at(sO, t, 4 * half + i), out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]);
+                    fence_proxy_async_smem();
+                    named_barrier(2, 32 * kOutWarps);
+                    if (issuer && !*abort_p) {
+                        tma_store_3d(&map_o, sm + kOutO, v0, g * R + r, (int)(sg.start + (int64_t)c * kTcC));
+                        bulk_commit_group();
+                    }
+                } else if (t < len_of(c)) {
+                    // a partial chunk ends inside the tile: rows one by one
+                    __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.o) +
+                                       ((sg.start + (int64_t)c * kTcC + t) * a.H + g * R + r) * (int64_t)a.V + v0 + 32 * half;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (8 * i < nv - 32 * half)
+                            reinterpret_cast<uint4*>(p)[i] = make_uint4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]);
                 }
             }
         }
+        if (issuer) bulk_wait_all();
     } else {
         // ------------------------------------------------------------ the state
         // Thread: state row k = 32 quarter + lane, 32 of the 64 V columns.
