@@ -55,14 +55,14 @@ ssd_status cuda_fail(cudaError_t e, const char* what) {
 // Per-kernel event timing (ssd_profile_enable / ssd_profile_read).
 enum Stage { ST_TABLE, ST_CUMSUM, ST_CHUNK_STATE, ST_STATE_PASSING, ST_CHUNK_SCAN, ST_STATE_UPDATE,
              ST_CONV, ST_CONV_UPDATE, ST_NORM, ST_STRICT_CUMSUM, ST_STRICT_STATE, ST_STRICT_PASSING,
-             ST_STRICT_SCAN, ST_STRICT_CACHE, ST_STRICT_UPDATE, ST_STRICT_FOLD, ST_LA_STATE, ST_LA_SCAN, ST_LA_UPDATE,
+             ST_STRICT_SCAN, ST_STRICT_CACHE, ST_STRICT_UPDATE, ST_STRICT_FOLD, ST_LA_STATE, ST_LA_PASSING, ST_LA_SCAN, ST_LA_UPDATE,
              ST_PAGES_PLAN, ST_PAGES_MOVE, ST_COUNT };
 const char* const kStageName[ST_COUNT] = {"ssd_chunk_table", "ssd_chunk_cumsum", "ssd_chunk_state",
                                           "ssd_state_passing", "ssd_chunk_scan", "ssd_state_update", "ssd_conv1d", "ssd_conv1d_update",
                                           "ssd_gated_rmsnorm", "ssd_strict_cumsum", "ssd_strict_chunk_state",
                                           "ssd_strict_state_passing", "ssd_strict_chunk_scan",
                                           "ssd_strict_cache_fill", "ssd_strict_state_update",
-                                          "ssd_strict_fold", "ssd_linear_attn_state", "ssd_linear_attn_scan",
+                                          "ssd_strict_fold", "ssd_linear_attn_state", "ssd_linear_attn_passing", "ssd_linear_attn_scan",
                                           "ssd_linear_attn_update", "ssd_pages_plan", "ssd_pages_move"};
 constexpr size_t kMaxRecords = 65536;
 
@@ -1579,6 +1579,12 @@ extern "C" ssd_status ssd_linear_attn_fwd(const void* q, const void* k, const vo
     if (two_pass) {
         const int64_t segs = cu_seqlens || p.bf16 ? p.max_segs : (int64_t)a.nseq * (a.nps - 1);
         s = launch_la<false>(p, segs, st);
+        ++n;
+    }
+    if (s == SSD_OK && many) {
+        StageScope sc(ST_LA_PASSING, st);
+        const dim3 grid((unsigned)a.nseq, (unsigned)a.Hk, (unsigned)((a.V * a.K + 4 * la::kPassThreads - 1) / (4 * la::kPassThreads)));
+        la::k_la_passing<<<grid, la::kPassThreads, 0, st>>>(a);
         ++n;
     }
     if (s == SSD_OK) {

@@ -52,9 +52,10 @@ struct Args {
 };
 
 // One segment: tokens [start, start + len) of the packed rows, number j of the n segments
-// of sequence seq, whose n + 1 state slots begin at slot0. Slot slot0 holds a copy of the
-// sequence's initial state (the state may be replaced in place while other segments'
-// CTAs still run), slot0 + i the state that segment i-1 alone adds.
+// of sequence seq, whose n + 1 state slots begin at slot0. After the state pass slot slot0
+// holds a copy of the sequence's initial state (the state may be replaced in place while other
+// segments' CTAs still run), slot0 + i the state that segment i-1 alone adds; the passing
+// kernel turns slots slot0 + 1 .. slot0 + n - 1 into the states entering segments 1 .. n-1.
 struct Seg {
     int32_t seq, j, n, slot0, len;
     int64_t start;
@@ -126,6 +127,46 @@ __device__ __forceinline__ void check_decay(float g) {
 }
 
 // ---------------------------------------------------------------------------------
+// States entering the segments, in place: S_j = lam^Ls S_(j-1) + (what segment j-1 adds), from
+// the copy of the initial state. One thread per four state elements, the loads of four
+// segments in flight ahead of the chain. (Each output CTA summing the segments before it
+// itself costs a pass over all their states per segment: with 64 segments the output pass took
+// ten times as long.)
+constexpr int kPassThreads = 256;
+
+__global__ void __launch_bounds__(kPassThreads) k_la_passing(const __grid_constant__ Args a) {
+    const int s = blockIdx.x, g = blockIdx.y;
+    const int e = 4 * (blockIdx.z * kPassThreads + threadIdx.x), size = a.V * a.K;
+    int first = s * a.nps, n = a.nps;
+    if (a.table) {
+        if (*a.count == 0) return;                                // a bad cu_seqlens
+        first = a.first[s];
+        n = a.first[s + 1] - first;
+    }
+    if (e >= size || n < 2) return;
+    const int64_t per_state = (int64_t)a.Hk * size;
+    float* p = a.slots + (int64_t)(first + s) * per_state + (int64_t)g * size + e;
+    const float2 lam = pow2f(a.log_decay[g], a.Ls);
+    const bool init = a.init && page_of(a.init_pages, a.npages, s) >= 0;
+    float4 x = init ? *reinterpret_cast<const float4*>(p) : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j = 1; j < n; j += 4) {
+        float4 y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (j + i < n) y[i] = *reinterpret_cast<const float4*>(p + (j + i) * per_state);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (j + i < n) {
+                x.x = fmaf(lam.x, x.x, fmaf(lam.y, x.x, y[i].x));
+                x.y = fmaf(lam.x, x.y, fmaf(lam.y, x.y, y[i].y));
+                x.z = fmaf(lam.x, x.z, fmaf(lam.y, x.z, y[i].z));
+                x.w = fmaf(lam.x, x.w, fmaf(lam.y, x.w, y[i].w));
+                *reinterpret_cast<float4*>(p + (j + i) * per_state) = x;
+            }
+    }
+}
+
+// ---------------------------------------------------------------------------------
 // CUDA-core prompt kernel for fp32 (FP32 arithmetic throughout; the tensor cores would round
 // the inputs). One CTA per (segment, key/value
 // head, 64 columns of V); chunks of 64 tokens in shared memory; the state in shared
@@ -157,14 +198,9 @@ __global__ void __launch_bounds__(kSimtThreads) k_la_simt(const __grid_constant_
     float* pw = sS + K * VB;                 // lam^0 .. lam^C
     float* sq = pw + C + 4;                  // [C][ldk]
     float* sP = sq + C * ldk;                // [C][C + 4]
-    __shared__ float2 lam_seg;
-
     const float gd = a.log_decay[g];
     if (tid <= C) pw[tid] = (float)pow_decay(gd, tid);
-    if (tid == 0) {
-        check_decay(gd);
-        lam_seg = pow2f(gd, a.Ls);
-    }
+    if (tid == 0) check_decay(gd);
     const int64_t per_state = (int64_t)a.Hk * V * K, head = ((int64_t)g * V + v0) * K;
     const int64_t ip = a.init ? page_of(a.init_pages, a.npages, sg.seq) : -1;
     const bool last = sg.j + 1 == sg.n;
@@ -184,9 +220,8 @@ __global__ void __launch_bounds__(kSimtThreads) k_la_simt(const __grid_constant_
         float s = 0.f;
         if (vv < nv) {
             if (OUT) {
-                if (ip >= 0) s = sg.n == 1 ? a.init[ip * per_state + at] : a.slots[(int64_t)sg.slot0 * per_state + at];
-                for (int i = 1; i <= sg.j; ++i)
-                    s = fmaf(lam_seg.x, s, fmaf(lam_seg.y, s, a.slots[(int64_t)(sg.slot0 + i) * per_state + at]));
+                if (sg.j > 0) s = a.slots[(int64_t)(sg.slot0 + sg.j) * per_state + at];
+                else if (ip >= 0) s = sg.n == 1 ? a.init[ip * per_state + at] : a.slots[(int64_t)sg.slot0 * per_state + at];
             } else if (sg.j == 0 && ip >= 0) {
                 a.slots[(int64_t)sg.slot0 * per_state + at] = a.init[ip * per_state + at];
             }

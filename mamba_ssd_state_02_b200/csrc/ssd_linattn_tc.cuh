@@ -7,7 +7,8 @@
 //   state pass: the FP32 state the segment adds, S' = lam^len S + K^T (w V) from S = 0, w_s =
 //       lam^(len-1-s). w V goes to the tensor cores as three bf16 terms (2^-24 of it: the
 //       final state is an FP32 output, and two terms would leave it at 2e-6 relative).
-//   output pass: starts from the states of the segments before it, and per chunk
+//   output pass: starts from the state entering the segment (the passing kernel in between
+//       makes it from what the segments before add), and per chunk
 //       P  = (Q K^T) o lam^(t-s), s <= t        UMMA -> TMEM, warps scale and mask, bf16 -> TMEM
 //       Oi = P V                                UMMA, A from TMEM
 //       Ox = Q [S_hi | S_lo]                    UMMA, N = 128; S = S_hi + S_lo, a bf16 pair
@@ -239,7 +240,8 @@ k_la_tc_state(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
             if (ip >= 0) {
                 const float* from = a.init + ip * per_state + head;
 #pragma unroll 4
-                for (int e = tid - 32 * (4 + kWriteWarps); e < nv * K; e += 32 * kStateWarps) slots[e] = from[e];
+                for (int e = 4 * (tid - 32 * (4 + kWriteWarps)); e < nv * K; e += 128 * kStateWarps)
+                    *reinterpret_cast<float4*>(slots + e) = *reinterpret_cast<const float4*>(from + e);
             }
         }
         float S[32];
@@ -338,7 +340,7 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
     __shared__ float pw[kTcC + 1];           // lam^0 .. lam^128
     __shared__ float pws[32 + kTcC];         // 32 zeros, then scale lam^0 .. lam^127
     __shared__ __align__(16) float rev[32];  // lam^31 .. lam^0
-    __shared__ float2 lam_full, lam_seg, lam_len;
+    __shared__ float2 lam_full, lam_len;
     // pairs for the two buffers of K, V, Q and the scores, then single barriers
     enum { FULL_K = 0, EMPTY_K = 2, FULL_V = 4, EMPTY_V = 6, FULL_Q = 8, EMPTY_Q = 10, QK_DONE = 12, P_READY = 14, O_DONE = 16,
            O_FREE = 18, QS_DONE, W_READY, D_DONE, D_FREE, S_READY, TAIL_READY, DRAINED, STALL = DRAINED + 3, BARS };
@@ -358,7 +360,6 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
         }
     }
     if (tid == 256) lam_full = pow2f(gd, kTcC);
-    if (tid == 288) lam_seg = pow2f(gd, a.Ls);
     if (tid == 320) lam_len = pow2f(gd, sg.len);
     if (tid < BARS) {
         const int pair = tid & ~1;
@@ -712,8 +713,8 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
         // chunks exchanged to spread the banks) to the threads that keep them.
         const uint32_t sS = smem_u32(sm + kOutS);
         if (has_init || fp >= 0) {
-            const float* slots = a.slots + (int64_t)sg.slot0 * per_state + head;
-            const float* first = a.two_pass ? slots : a.init + ip * per_state + head;
+            const float* slots = a.slots + (int64_t)(sg.slot0 + sg.j) * per_state + head;
+            const float* from = a.two_pass ? slots : a.init + ip * per_state + head;
             float* fin = a.fin + fp * per_state + head;
             const int w8 = warp - (4 + kScoreWarps + kOutWarps);
 #pragma unroll 1
@@ -724,20 +725,15 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
                 for (int i = 0; i < 8; ++i) {
                     const int v = w8 + 8 * (2 * step + (i >> 2)), kk = lane + 32 * (i & 3);
                     at[i] = v < nv && kk < K ? v * K + kk : -1;
-                    x[i] = ip >= 0 && at[i] >= 0 ? first[at[i]] : 0.f;
+                    x[i] = has_init && at[i] >= 0 ? from[at[i]] : 0.f;
                 }
-#pragma unroll 1
-                for (int j = 1; j <= sg.j; ++j)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (at[i] >= 0) x[i] = fmaf(lam_seg.x, x[i], fmaf(lam_seg.y, x[i], slots[j * per_state + at[i]]));
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int v = w8 + 8 * (2 * step + (i >> 2)), kk = lane + 32 * (i & 3);
                     const uint32_t to = sS + kk * 256 + ((((uint32_t)v >> 2) ^ (kk & 15)) << 4) + (v & 3) * 4;
                     asm volatile("st.shared.f32 [%0], %1;" ::"r"(to), "f"(x[i]) : "memory");
                     if (fp >= 0 && at[i] >= 0)
-                        fin[at[i]] = fmaf(lam_len.x, x[i], fmaf(lam_len.y, x[i], slots[(sg.j + 1) * per_state + at[i]]));
+                        fin[at[i]] = fmaf(lam_len.x, x[i], fmaf(lam_len.y, x[i], slots[per_state + at[i]]));
                 }
             }
             named_barrier(1, 32 * kStateWarps);
