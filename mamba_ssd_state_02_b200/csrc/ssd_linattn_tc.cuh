@@ -72,14 +72,33 @@ __device__ __forceinline__ float2 fadd2(float2 x, float2 y) {
 __device__ __forceinline__ uint32_t tile_at(uint32_t base, int r, int c) { return base + tc::swz(r, c); }
 
 // ---------------------------------------------------------------------------------
+// A matrix descriptor's low word: start address, and the distance between 64-wide blocks of an
+// MN-major operand (not read for K-major ones). The high word is the same for all. In
+// units of 16 bytes, a K-step of 16 advances a K-major operand by 2, the other half of its
+// columns lies 1024 on, and a K-step of an MN-major operand is 128.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t block = 16384) {
+    return (saddr >> 4) | (block >> 4) << 16;
+}
+constexpr uint32_t kDescHi = (1024 >> 4) | 1u << 14 | 2u << 29;          // SBO, version, 128-byte swizzle
+
+__device__ __forceinline__ void umma(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool accumulate) {
+    const uint64_t hi = (uint64_t)kDescHi << 32;
+    tc::umma_bf16(d, hi | a_lo, hi | b_lo, idesc, accumulate);
+}
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, bool accumulate) {
+    tc::umma_bf16_ts(d, a_tmem, (uint64_t)kDescHi << 32 | b_lo, idesc, accumulate);
+}
+
+// ---------------------------------------------------------------------------------
 // State pass. Warp 0 issues the TMA loads, warp 2 the UMMAs; eight warps write w V, eight hold
-// the state. K, V, w V and D are double-buffered by chunk, and one barrier says that a chunk's
-// UMMAs are done: its K, V and w V buffers are free and its D is ready. The three terms of w V
-// lie side by side as one N = 192 operand, so K is read once for them (97 cycles a step; three
-// N = 64 steps take 147, bound by the reads of their operands).
+// the state. K and V are triple-buffered; w V goes through two buffers of 64 tokens, so
+// that one is written while the UMMAs read the other; D is double-buffered. The three terms of
+// w V lie side by side as one N = 192 operand, so K is read once for them (97 cycles a step;
+// three N = 64 steps take 147, bound by the reads of their operands).
 constexpr int kWriteWarps = 8;
+constexpr int kHalf = 64;                    // tokens of a w V buffer
 constexpr int kStateThreads = 32 * (4 + kWriteWarps + kStateWarps);
-constexpr int kStateV = 65536, kStateW = 98304;          // K at 0: 2 x 32 KB; V: 2 x 16 KB; w V: 2 x 48 KB
+constexpr int kStateV = 98304, kStateW = 147456;         // K at 0: 3 x 32 KB; V: 3 x 16 KB; w V: 2 x 24 KB
 constexpr int kStateSmem = 196608 + 1024;
 
 __global__ void __launch_bounds__(kStateThreads, 1)
@@ -90,18 +109,16 @@ k_la_tc_state(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
     const int vb = blockIdx.x % nvb, g = (blockIdx.x / nvb) % a.Hk;
     Seg sg;
     if (!find_seg(a, blockIdx.x / nvb / a.Hk, true, &sg)) return;
-    const int K = a.K, v0 = vb * kTcV, nv = min(kTcV, a.V - v0), halves = (K + 63) / 64;
-    const int nt = (sg.len + kTcC - 1) / kTcC;
-    auto len_of = [&](int c) { return min(kTcC, sg.len - c * kTcC); };
-    auto steps_of = [&](int c) { return (len_of(c) + 15) / 16; };
+    const int K = a.K, v0 = vb * kTcV, nv = min(kTcV, a.V - v0), tiles = (K + 63) / 64;
+    const int nt = (sg.len + kTcC - 1) / kTcC, nh = (sg.len + kHalf - 1) / kHalf;
 
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ float pw[kTcC + 1];
     __shared__ float2 lam_full, lam_tail;
-    __shared__ uint64_t bars[10];
-    uint64_t *full = bars, *done = bars + 2, *w_ready = bars + 4, *d_free = bars + 6;
-    uint64_t &drained = bars[8], &stall_bar = bars[9];
+    // FULL, FREE: K and V of a chunk; W_*: w V of a half; D_*: D of a chunk
+    enum { FULL = 0, FREE = 3, W_READY = 6, W_FREE = 8, D_DONE = 10, D_FREE = 12, DRAINED = 14, STALL, BARS };
+    __shared__ uint64_t bars[BARS];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
 
@@ -109,8 +126,11 @@ k_la_tc_state(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
     const float gd = a.log_decay[g];
     if (tid <= kTcC) pw[tid] = (float)pow_decay(gd, tid);
     if (tid == 160) lam_full = pow2f(gd, kTcC);
-    if (tid == 192) lam_tail = pow2f(gd, nt > 0 ? len_of(nt - 1) : 0);
-    if (tid < 10) mbar_init(&bars[tid], tid == 4 || tid == 5 ? kWriteWarps : tid == 6 || tid == 7 ? kStateWarps : 1);
+    if (tid == 192) lam_tail = pow2f(gd, nt > 0 ? sg.len - (nt - 1) * kTcC : 0);
+    if (tid < BARS) {
+        const int pair = tid & ~1;
+        mbar_init(&bars[tid], pair == W_READY ? kWriteWarps : pair == D_FREE ? kStateWarps : 1);
+    }
     if (tid == 0) {
         check_decay(gd);
         abort_flag = 0;
@@ -134,100 +154,122 @@ k_la_tc_state(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
             prefetch_tmap(&map_v);
             int n = 0;
 #pragma unroll 1
-            for (int c = 0; c < nt; ++c) {
-                const int b = c & 1, t0 = (int)(sg.start + (int64_t)c * kTcC);
-                if (c + 1 < nt) {            // the next chunk into L2 meanwhile
-#pragma unroll 1
-                    for (int h = 0; h < halves; ++h) tma_prefetch_3d(&map_k, 64 * h, g, t0 + kTcC);
-                    tma_prefetch_3d(&map_v, v0, g, t0 + kTcC);
-                }
-                if (c >= 2) wait_bar(&done[b], (c >> 1) - 1, abort_p);
+            for (int c = 0, b = 0, ph = 0; c < nt; ++c) {
+                const int t0 = (int)(sg.start + (int64_t)c * kTcC);
+                if (c >= 3) wait_bar(&bars[FREE + b], ph - 1, abort_p);
                 if (*abort_p) break;
-                mbar_arrive_expect_tx(&full[b], (halves + 1) * 16384);
+                mbar_arrive_expect_tx(&bars[FULL + b], (tiles + 1) * 16384);
 #pragma unroll 1
-                for (int h = 0; h < halves; ++h) tma_load_3d(sm + b * 32768 + h * 16384, &map_k, &full[b], 64 * h, g, t0);
-                tma_load_3d(sm + kStateV + b * 16384, &map_v, &full[b], v0, g, t0);
+                for (int t = 0; t < tiles; ++t) tma_load_3d(sm + b * 32768 + t * 16384, &map_k, &bars[FULL + b], 64 * t, g, t0);
+                tma_load_3d(sm + kStateV + b * 16384, &map_v, &bars[FULL + b], v0, g, t0);
                 ++n;
+                if (++b == 3) {
+                    b = 0;
+                    ++ph;
+                }
             }
             // The last phase issued on each barrier completes once its bytes have landed (a
             // phase is issued only after the previous one has been consumed).
-            for (int i = 0; i < 2; ++i)
-                if (n > i) mbar_wait(&full[i], ((n - 1 - i) >> 1) & 1);
+            for (int b = 0; b < 3; ++b)
+                if (n > b) mbar_wait(&bars[FULL + b], ((n - 1 - b) / 3) & 1);
         }
     } else if (warp == 2) {
         // ------------------------------------------------------------ UMMA issuer
         // D (k x [v hi | v mid | v lo]) = K^T (w V): A = K, MN-major; B = w V, MN-major.
         const uint32_t id = idesc_bf16(128, 192, 1, 1);
-        const uint64_t dK = smem_desc(smem_u32(sm), 16384, 1024), dW = smem_desc(smem_u32(sm + kStateW), 16384, 1024);
-        if (a.stall) wait_bar(&stall_bar, 0, abort_p);            // test hook: a wait that runs out
+        const uint32_t dK = desc_lo(smem_u32(sm)), dW = desc_lo(smem_u32(sm + kStateW), 8192);
+        if (a.stall) wait_bar(&bars[STALL], 0, abort_p);          // test hook: a wait that runs out
+        bool ok = true;
 #pragma unroll 1
-        for (int c = 0; c < nt; ++c) {
-            const int b = c & 1, ph = c >> 1;
-            wait_bar(&full[b], ph, abort_p);
-            wait_bar(&w_ready[b], ph, abort_p);
-            if (c >= 2) wait_bar(&d_free[b], ph - 1, abort_p);
-            if (!go_on(abort_p)) break;
-            tc_fence_after();
-            const uint64_t dk = desc_add(dK, b * 32768), dw = desc_add(dW, b * 49152);
-            const uint32_t d = tD + 256 * b;
-            const int steps = steps_of(c);
-            if (elect_one()) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (k < steps) umma_bf16(d, desc_add(dk, k * kMnStep), desc_add(dw, k * kMnStep), id, k > 0);
-                umma_commit(&done[b]);
+        for (int c = 0, b = 0, ph = 0, h = 0; c < nt && ok; ++c) {
+            wait_bar(&bars[FULL + b], ph, abort_p);
+            if (c >= 2) wait_bar(&bars[D_FREE + (c & 1)], (c >> 1) - 1, abort_p);
+            const uint32_t d = tD + 256 * (c & 1);
+#pragma unroll 1
+            for (int i = 0; i < 2 && h < nh; ++i, ++h) {
+                wait_bar(&bars[W_READY + (h & 1)], h >> 1, abort_p);
+                if (!(ok = go_on(abort_p))) break;
+                tc_fence_after();
+                const uint32_t dk = dK + b * 2048 + i * 512, dw = dW + (h & 1) * 1536;
+                const int steps = min(4, (sg.len - h * kHalf + 15) / 16);
+                if (elect_one()) {
+#pragma unroll 1
+                    for (int k = 0; k < steps; ++k) umma(d, dk + k * 128, dw + k * 128, id, i + k > 0);
+                    umma_commit(&bars[W_FREE + (h & 1)]);
+                    if (i == 1 || h + 1 == nh) {
+                        umma_commit(&bars[D_DONE + (c & 1)]);
+                        umma_commit(&bars[FREE + b]);
+                    }
+                }
+                __syncwarp();
             }
-            __syncwarp();
+            if (++b == 3) {
+                b = 0;
+                ++ph;
+            }
         }
         // Every MMA issued above has completed once this commit arrives.
-        if (elect_one()) umma_commit(&drained);
+        if (elect_one()) umma_commit(&bars[DRAINED]);
         __syncwarp();
-        mbar_wait(&drained, 0);
+        mbar_wait(&bars[DRAINED], 0);
     } else if (warp < 4) {
         // nothing: the groups below start at a multiple of four warps (TMEM lane quarters)
     } else if (warp < 4 + kWriteWarps) {
         // ------------------------------------------------------------ w V
-        // Thread: token rows wt + 32 i of a chunk, 8 columns.
-        const int wi = tid - 128, wt = wi >> 3, wc = wi & 7;
+        // Thread: token rows wt and wt + 32 of a half, 8 columns. Factors and addresses are the
+        // same in every full chunk.
+        const int wt = (tid - 128) >> 3, wc = tid & 7;
+        const uint32_t at = tile_at(smem_u32(sm), wt, wc);        // row wt + 32 i is 4096 i further
+        float w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = pw[kTcC - 1 - wt - 32 * i];
 #pragma unroll 1
-        for (int c = 0; c < nt; ++c) {
-            const int b = c & 1, len = len_of(c), rows = 16 * steps_of(c);
-            wait_bar(&full[b], (c >> 1) & 1, abort_p);
-            if (c >= 2) wait_bar(&done[b], ((c >> 1) - 1) & 1, abort_p);
-            const uint32_t sv = smem_u32(sm + kStateV) + b * 16384, sw = smem_u32(sm + kStateW) + b * 49152;
+        for (int c = 0, b = 0, ph = 0; c < nt; ++c) {
+            const int len = sg.len - c * kTcC;                    // tokens from the chunk on
+            if (len < kTcC)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int s = wt + 32 * i;
-                if (s >= rows) break;
-                uint32_t y[3][4];
-                if (s < len) {
-                    const uint4 x = ld_shared_v4(tile_at(sv, s, wc));
-                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-                    const float w = pw[len - 1 - s];
+                for (int i = 0; i < 4; ++i) w[i] = pw[max(0, len - 1 - wt - 32 * i)];
+            wait_bar(&bars[FULL + b], ph, abort_p);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float2 z = fmul2(bf16x2_to_f2(xs[e]), make_float2(w, w));
+            for (int i = 0; i < 2; ++i) {
+                if (i * kHalf >= len) break;
+                if (c > 0) wait_bar(&bars[W_FREE + i], c - 1, abort_p);
+                const uint32_t from = at + kStateV + b * 16384 + i * 8192, to = at + kStateW + i * 24576;
 #pragma unroll
-                        for (int n = 0; n < 3; ++n) {
-                            y[n][e] = pack_bf16(z);
-                            z = fsub2(z, bf16x2_to_f2(y[n][e]));
+                for (int r = 0; r < 2; ++r) {
+                    const int left = len - i * kHalf - wt - 32 * r;
+                    uint32_t y[3][4] = {};
+                    if (left > 0) {
+                        const uint4 x = ld_shared_v4(from + r * 4096);
+                        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+                        const float2 ww = make_float2(w[2 * i + r], w[2 * i + r]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float2 z = fmul2(bf16x2_to_f2(xs[e]), ww);
+#pragma unroll
+                            for (int n = 0; n < 3; ++n) {
+                                y[n][e] = pack_bf16(z);
+                                z = fsub2(z, bf16x2_to_f2(y[n][e]));
+                            }
                         }
+                    } else {
+                        // Rows past the sequence's end (another sequence's, or nothing): zero in
+                        // w V and in K, since 0 times what K holds need not be 0.
+                        for (int t = 0; t < tiles; ++t)
+                            st_shared_v4(at + b * 32768 + t * 16384 + i * 8192 + r * 4096, 0, 0, 0, 0);
                     }
-                } else {
-                    // Rows past the sequence's end (another sequence's, or nothing): zero in w V
-                    // and in K, since 0 times what K holds there need not be 0.
 #pragma unroll
-                    for (int n = 0; n < 3; ++n) y[n][0] = y[n][1] = y[n][2] = y[n][3] = 0;
-#pragma unroll 1
-                    for (int h = 0; h < halves; ++h)
-                        st_shared_v4(tile_at(smem_u32(sm) + b * 32768 + h * 16384, s, wc), 0, 0, 0, 0);
+                    for (int n = 0; n < 3; ++n)
+                        st_shared_v4(to + r * 4096 + n * 8192, y[n][0], y[n][1], y[n][2], y[n][3]);
                 }
-#pragma unroll
-                for (int n = 0; n < 3; ++n) st_shared_v4(tile_at(sw + n * 16384, s, wc), y[n][0], y[n][1], y[n][2], y[n][3]);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[W_READY + i]);
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&w_ready[b]);
+            if (++b == 3) {
+                b = 0;
+                ++ph;
+            }
         }
     } else {
         // ------------------------------------------------------------ the state
@@ -244,16 +286,17 @@ k_la_tc_state(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
                     *reinterpret_cast<float4*>(slots + e) = *reinterpret_cast<const float4*>(from + e);
             }
         }
-        float S[32];
+        float2 S[16];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) S[i] = 0.f;
+        for (int i = 0; i < 16; ++i) S[i] = make_float2(0.f, 0.f);
 #pragma unroll 1
         for (int c = 0; c < nt; ++c) {
             const int b = c & 1;
-            wait_bar(&done[b], (c >> 1) & 1, abort_p);
+            wait_bar(&bars[D_DONE + b], c >> 1, abort_p);
             tc_fence_after();
             const uint32_t t = tD + 256 * b + ((uint32_t)quarter << 21) + 32 * half;
             const float2 lam = c == nt - 1 ? lam_tail : lam_full;
+            const float2 hi = make_float2(lam.x, lam.x), lo = make_float2(lam.y, lam.y);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 uint32_t d[3][16];
@@ -263,13 +306,13 @@ k_la_tc_state(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
                 if (e == 1) {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&d_free[b]);
+                    if (lane == 0) mbar_arrive(&bars[D_FREE + b]);
                 }
+                auto two = [&](int n, int i) { return make_float2(__uint_as_float(d[n][2 * i]), __uint_as_float(d[n][2 * i + 1])); };
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float& s = S[16 * e + i];
-                    const float x = __uint_as_float(d[0][i]) + (__uint_as_float(d[1][i]) + __uint_as_float(d[2][i]));
-                    s = fmaf(lam.x, s, fmaf(lam.y, s, x));
+                for (int i = 0; i < 8; ++i) {
+                    float2& s = S[8 * e + i];
+                    s = ffma2(hi, s, ffma2(lo, s, fadd2(two(0, i), fadd2(two(1, i), two(2, i)))));
                 }
             }
         }
@@ -278,7 +321,7 @@ k_la_tc_state(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
         const int rows = k < K ? nv - 32 * half : 0;
 #pragma unroll
         for (int i = 0; i < 32; ++i, p += K)
-            if (i < rows) *p = S[i];
+            if (i < rows) *p = i & 1 ? S[i / 2].y : S[i / 2].x;
     }
     tc_fence_before();
     __syncthreads();
@@ -299,21 +342,6 @@ k_la_tc_state(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
 // and [128, 256) (units alternate), P of a 32-token block in the first 16 columns of the
 // block's scores (read and written by the same thread), Oi [256, 320), Ox [320, 448), D
 // [448, 512).
-
-// A matrix descriptor's low word: start address, and the distance between 64-wide blocks of an
-// MN-major operand (16 KB; not read for K-major ones). The high word is the same for all. In
-// units of 16 bytes, a K-step of 16 advances a K-major operand by 2, the other half of its
-// columns lies 1024 on, and a K-step of an MN-major operand is 128.
-__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return (saddr >> 4) | (16384u >> 4) << 16; }
-constexpr uint32_t kDescHi = (1024 >> 4) | 1u << 14 | 2u << 29;          // SBO, version, 128-byte swizzle
-
-__device__ __forceinline__ void umma(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool accumulate) {
-    const uint64_t hi = (uint64_t)kDescHi << 32;
-    tc::umma_bf16(d, hi | a_lo, hi | b_lo, idesc, accumulate);
-}
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, bool accumulate) {
-    tc::umma_bf16_ts(d, a_tmem, (uint64_t)kDescHi << 32 | b_lo, idesc, accumulate);
-}
 
 constexpr int kScoreWarps = 8, kOutWarps = 8;
 constexpr int kOutThreads = 32 * (4 + kScoreWarps + kOutWarps + kStateWarps);
