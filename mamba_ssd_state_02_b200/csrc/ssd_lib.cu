@@ -1322,9 +1322,9 @@ struct LaPlan {
 };
 
 // Segment length in tokens (a multiple of 128). A pass's CTAs, one per (segment, key/value
-// head, 64 columns of V), run in waves of one per SM; a CTA costs its chunks times the query
-// heads plus about two chunks of prologue and epilogue, in the state pass half a chunk per
-// chunk. Dense: the number of segments per sequence with the least cost. Packed (lengths known
+// head, 64 columns of V), run in waves of one per SM; a CTA of the output pass costs its chunks
+// times the query heads plus about five of those units to start and end, one of the state pass
+// 0.6 of a unit a chunk and three to start and end (measured: 2 and 1.2 us, 10 and 5 us). Dense: the number of segments per sequence with the least cost. Packed (lengths known
 // on the device only): the same with the mean length, where the longest segments are what the
 // last wave waits for.
 int la_segment_tokens(const LaPlan& p) {
@@ -1339,7 +1339,7 @@ int la_segment_tokens(const LaPlan& p) {
         for (int64_t n = 1; n <= std::min<int64_t>(nch, 64); ++n) {
             const int64_t m = (nch + n - 1) / n, segs = (nch + m - 1) / m;
             const double waves = (double)((a.nseq * segs * heads + nsm - 1) / nsm);
-            const double c = waves * (double)(m * a.R + 2) + waves * (0.5 * (double)m + 2);
+            const double c = waves * ((double)(m * a.R) + 5) + waves * (0.6 * (double)m + 3);
             if (n == 1 || c < best) {
                 best = c;
                 ls = m;
@@ -1351,8 +1351,8 @@ int la_segment_tokens(const LaPlan& p) {
     double best = 0;
     int64_t ls = 2;
     for (int64_t m = 2; m <= 8192; m *= 2) {
-        const double longest = std::min<double>((double)m, 2 * mean), cost = a.R + 0.5;
-        const double c = U * cost + longest * cost + 4 * U / std::min<double>((double)m, mean);
+        const double longest = std::min<double>((double)m, 2 * mean), cost = a.R + 0.6;
+        const double c = U * cost + 0.5 * longest * cost + 8 * U / std::min<double>((double)m, mean);
         if (m == 2 || c < best) {
             best = c;
             ls = m;

@@ -56,6 +56,20 @@ __device__ __forceinline__ void wait_bar(uint64_t* bar, uint32_t parity, volatil
         }
 }
 
+// The barrier at the start of a block: every warp has set up its part (barriers, tables, TMEM).
+// Warp 0 made the barriers itself and needs nothing else, so that its first loads are on their
+// way while the others still compute tables.
+__device__ __forceinline__ void start_block(int warp, int threads) {
+    tc::tc_fence_before();
+    if (warp == 0) {
+        __syncwarp();
+        asm volatile("bar.arrive 15, %0;" ::"r"(threads) : "memory");
+    } else {
+        tc::named_barrier(15, threads);
+    }
+    tc::tc_fence_after();
+}
+
 // For an issuing warp, after its waits: none of them was given up.
 __device__ __forceinline__ bool go_on(volatile int* abort_flag) { return __all_sync(0xffffffffu, *abort_flag == 0); }
 
@@ -124,9 +138,10 @@ k_la_tc_state(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const float gd = a.log_decay[g];
-    if (tid <= kTcC) pw[tid] = (float)pow_decay(gd, tid);
-    if (tid == 160) lam_full = pow2f(gd, kTcC);
-    if (tid == 192) lam_tail = pow2f(gd, nt > 0 ? sg.len - (nt - 1) * kTcC : 0);
+    const int tt = tid - 64;                 // warps 0 and 1 have other things to set up
+    if (tt >= 0 && tt <= kTcC) pw[tt] = (float)pow_decay(gd, tt);
+    if (tid == 256) lam_full = pow2f(gd, kTcC);
+    if (tid == 288) lam_tail = pow2f(gd, nt > 0 ? sg.len - (nt - 1) * kTcC : 0);
     if (tid < BARS) {
         const int pair = tid & ~1;
         mbar_init(&bars[tid], pair == W_READY ? kWriteWarps : pair == D_FREE ? kStateWarps : 1);
@@ -140,9 +155,7 @@ k_la_tc_state(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
         tmem_alloc(&tmem_slot, 512);
         tmem_relinquish();
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
+    start_block(warp, kStateThreads);
     const uint32_t tD = tmem_slot;           // 192 columns at 0 and at 256
     volatile int* abort_p = &abort_flag;
     const int64_t per_state = (int64_t)a.Hk * a.V * K, head = ((int64_t)g * a.V + v0) * K;
@@ -378,13 +391,14 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const float gd = a.log_decay[g];
-    if (tid <= kTcC) {
-        const float x = (float)pow_decay(gd, tid);
-        pw[tid] = x;
-        if (tid < kTcC) pws[32 + tid] = a.scale * x;
-        if (tid < 32) {
-            pws[tid] = 0.f;
-            rev[31 - tid] = x;
+    const int tt = tid - 64;                 // warps 0 and 1 have other things to set up
+    if (tt >= 0 && tt <= kTcC) {
+        const float x = (float)pow_decay(gd, tt);
+        pw[tt] = x;
+        if (tt < kTcC) pws[32 + tt] = a.scale * x;
+        if (tt < 32) {
+            pws[tt] = 0.f;
+            rev[31 - tt] = x;
         }
     }
     if (tid == 256) lam_full = pow2f(gd, kTcC);
@@ -414,9 +428,7 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
             fp = -1;
         }
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
+    start_block(warp, kOutThreads);
     const uint32_t tbase = tmem_slot, tOi = tbase + 256, tOx = tbase + 320, tD = tbase + 448;
     volatile int* abort_p = &abort_flag;
     const bool has_init = ip >= 0 || sg.j > 0;                    // the first chunk meets a state
@@ -736,7 +748,7 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
         // Thread: state row k = 32 quarter + lane, 32 of the 64 V columns.
         const int quarter = warp & 3, half = (warp - 4 - kScoreWarps - kOutWarps) >> 2, k = 32 * quarter + lane;
         // The state entering the segment, and the final state after the last one: a warp takes
-        // columns of V one by one, lanes side by side along K, eight elements a lane in flight;
+        // columns of V one by one, lanes side by side along K, sixteen elements a lane in flight;
         // then through shared memory (the place of the operand S; rows of 64 floats, 16-byte
         // chunks exchanged to spread the banks) to the threads that keep them.
         const uint32_t sS = smem_u32(sm + kOutS);
@@ -746,22 +758,20 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
             float* fin = a.fin + fp * per_state + head;
             const int w8 = warp - (4 + kScoreWarps + kOutWarps);
 #pragma unroll 1
-            for (int step = 0; step < 4; ++step) {
-                float x[8];
-                int at[8];
+            for (int step = 0; step < 2; ++step) {
+                float x[16];
+                auto v_of = [&](int i) { return w8 + 8 * (4 * step + (i >> 2)); };
+                auto k_of = [&](int i) { return lane + 32 * (i & 3); };
+                auto mine = [&](int i) { return v_of(i) < nv && k_of(i) < K; };
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int v = w8 + 8 * (2 * step + (i >> 2)), kk = lane + 32 * (i & 3);
-                    at[i] = v < nv && kk < K ? v * K + kk : -1;
-                    x[i] = has_init && at[i] >= 0 ? from[at[i]] : 0.f;
-                }
+                for (int i = 0; i < 16; ++i) x[i] = has_init && mine(i) ? from[v_of(i) * K + k_of(i)] : 0.f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int v = w8 + 8 * (2 * step + (i >> 2)), kk = lane + 32 * (i & 3);
+                for (int i = 0; i < 16; ++i) {
+                    const int v = v_of(i), kk = k_of(i);
                     const uint32_t to = sS + kk * 256 + ((((uint32_t)v >> 2) ^ (kk & 15)) << 4) + (v & 3) * 4;
                     asm volatile("st.shared.f32 [%0], %1;" ::"r"(to), "f"(x[i]) : "memory");
-                    if (fp >= 0 && at[i] >= 0)
-                        fin[at[i]] = fmaf(lam_len.x, x[i], fmaf(lam_len.y, x[i], slots[per_state + at[i]]));
+                    if (fp >= 0 && mine(i))
+                        fin[v * K + kk] = fmaf(lam_len.x, x[i], fmaf(lam_len.y, x[i], slots[per_state + v * K + kk]));
                 }
             }
             named_barrier(1, 32 * kStateWarps);
