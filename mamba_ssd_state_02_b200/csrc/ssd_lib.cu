@@ -1326,12 +1326,15 @@ struct LaPlan {
 // times the query heads plus about five of those units to start and end, one of the state pass
 // 0.6 of a unit a chunk and three to start and end (measured: 2 and 1.2 us, 10 and 5 us). Dense: the number of segments per sequence with the least cost. Packed (lengths known
 // on the device only): the same with the mean length, where the longest segments are what the
-// last wave waits for.
+// last wave waits for. The CUDA-core kernel has two CTAs per SM where their shared memory fits,
+// and no state pass for a single segment.
 int la_segment_tokens(const LaPlan& p) {
     constexpr int64_t kC = 128;
     const la::Args& a = p.a;
     if (const int v = g_segment_override.load()) return v;
-    const int64_t nsm = sm_count(), heads = (int64_t)a.Hk * ((a.V + 63) / 64);
+    const bool two = !p.bf16 && la::simt_smem(a.K, true) <= 112 * 1024;
+    const int64_t nsm = sm_count() * (two ? 2 : 1), heads = (int64_t)a.Hk * ((a.V + 63) / 64);
+    const double start = p.bf16 ? 5 : 1, state_start = p.bf16 ? 3 : 1;
     if (!p.varlen) {
         const int64_t nch = std::max<int64_t>(1, (a.seqlen + kC - 1) / kC);
         double best = 0;
@@ -1339,7 +1342,9 @@ int la_segment_tokens(const LaPlan& p) {
         for (int64_t n = 1; n <= std::min<int64_t>(nch, 64); ++n) {
             const int64_t m = (nch + n - 1) / n, segs = (nch + m - 1) / m;
             const double waves = (double)((a.nseq * segs * heads + nsm - 1) / nsm);
-            const double c = waves * ((double)(m * a.R) + 5) + waves * (0.6 * (double)m + 3);
+            double c = waves * ((double)(m * a.R) + start);
+            if (p.bf16 || segs > 1) c += waves * (0.6 * (double)m + state_start);
+            if (segs > 1) c += 1;
             if (n == 1 || c < best) {
                 best = c;
                 ls = m;
@@ -1352,7 +1357,7 @@ int la_segment_tokens(const LaPlan& p) {
     int64_t ls = 2;
     for (int64_t m = 2; m <= 8192; m *= 2) {
         const double longest = std::min<double>((double)m, 2 * mean), cost = a.R + 0.6;
-        const double c = U * cost + 0.5 * longest * cost + 8 * U / std::min<double>((double)m, mean);
+        const double c = U * cost + 0.5 * longest * cost + (start + state_start) * U / std::min<double>((double)m, mean);
         if (m == 2 || c < best) {
             best = c;
             ls = m;

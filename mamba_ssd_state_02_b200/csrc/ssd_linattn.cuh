@@ -168,185 +168,201 @@ __global__ void __launch_bounds__(kPassThreads) k_la_passing(const __grid_consta
 
 // ---------------------------------------------------------------------------------
 // CUDA-core prompt kernel for fp32 (FP32 arithmetic throughout; the tensor cores would round
-// the inputs). One CTA per (segment, key/value
-// head, 64 columns of V); chunks of 64 tokens in shared memory; the state in shared
-// memory as [K][64]. Without OUT: only the state that the segment adds.
+// the inputs). One CTA per (segment, key/value head, 64 columns of V); chunks of 64 tokens in
+// shared memory, the state there too as [K][64]. Without OUT: only the state that the segment
+// adds. Every product runs in 4 x 4 register tiles fed by 16-byte shared loads along the
+// summed index, eight for 64 FMAs.
 constexpr int kSimtC = 64;           // tokens per chunk
 constexpr int kSimtV = 64;           // V columns per CTA
 constexpr int kSimtThreads = 256;
 
-__host__ __device__ constexpr int simt_ld(int K) { return K + 4; }   // row stride: no bank conflict of 8 rows
+__host__ __device__ constexpr int simt_ld(int n) { return n + 4; }   // row stride: rows start in other banks
 __host__ __device__ constexpr size_t simt_smem(int K, bool out) {
-    return sizeof(float) * ((size_t)(out ? 2 : 1) * kSimtC * simt_ld(K) + kSimtC * kSimtV + (size_t)K * kSimtV +
-                            (out ? kSimtC * (kSimtC + 4) : 0) + kSimtC + 4);
+    return sizeof(float) * ((size_t)kSimtC * simt_ld(K) + kSimtC * kSimtV + (size_t)K * kSimtV + kSimtC + 4 +
+                            (out ? (size_t)kSimtC * simt_ld(K) + kSimtC * kSimtV + kSimtC * simt_ld(kSimtC) : 0));
+}
+
+// Rows [0, 64) of a [tokens][n] matrix (n a multiple of 8, `stride` elements between rows) into
+// shared memory with row stride ld; rows from len on are zeros. SCALE: row s times f[len-1-s].
+template <bool SCALE>
+__device__ __forceinline__ void simt_rows(float* dst, int ld, const float* src, int64_t stride, int n, int len, const float* f) {
+    const int per = n / 4;
+    for (int e = threadIdx.x; e < kSimtC * per; e += kSimtThreads) {
+        const int t = e / per, c4 = e - t * per;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (t < len) x = *reinterpret_cast<const float4*>(src + t * stride + 4 * c4);
+        if (SCALE) {
+            const float w = t < len ? f[len - 1 - t] : 0.f;
+            x = make_float4(w * x.x, w * x.y, w * x.z, w * x.w);
+        }
+        *reinterpret_cast<float4*>(dst + t * ld + 4 * c4) = x;
+    }
+}
+
+__device__ __forceinline__ void axpy4(float4& acc, float x, const float4& y) {
+    acc.x = fmaf(x, y.x, acc.x);
+    acc.y = fmaf(x, y.y, acc.y);
+    acc.z = fmaf(x, y.z, acc.z);
+    acc.w = fmaf(x, y.w, acc.w);
+}
+
+// acc[i] += sum over n of x[row i][n] * y[n][four columns], n in steps of four up to `end`.
+__device__ __forceinline__ void simt_tile(float4 (&acc)[4], const float* x, int ldx16, const float* y, int ldy, int end) {
+#pragma unroll 2
+    for (int n = 0; n < end; n += 4) {
+        float4 a[4], b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            a[i] = *reinterpret_cast<const float4*>(x + i * ldx16 + n);
+            b[i] = *reinterpret_cast<const float4*>(y + (n + i) * ldy);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            axpy4(acc[i], a[i].x, b[0]);
+            axpy4(acc[i], a[i].y, b[1]);
+            axpy4(acc[i], a[i].z, b[2]);
+            axpy4(acc[i], a[i].w, b[3]);
+        }
+    }
 }
 
 template <bool OUT>
-__global__ void __launch_bounds__(kSimtThreads) k_la_simt(const __grid_constant__ Args a) {
-    constexpr int C = kSimtC, VB = kSimtV, NT = kSimtThreads;
+__global__ void __launch_bounds__(kSimtThreads, 2) k_la_simt(const __grid_constant__ Args a) {
+    constexpr int C = kSimtC, VB = kSimtV, NT = kSimtThreads, ldp = simt_ld(C);
     const int nvb = (a.V + VB - 1) / VB;
     const int vb = blockIdx.x % nvb, g = (blockIdx.x / nvb) % a.Hk;
     Seg sg;
     if (!find_seg(a, blockIdx.x / nvb / a.Hk, OUT, &sg)) return;
-    const int K = a.K, V = a.V, ldk = simt_ld(K), tid = threadIdx.x;
+    const int K = a.K, V = a.V, ldk = simt_ld(K), tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int v0 = vb * VB, nv = min(VB, V - v0);
 
     extern __shared__ __align__(16) float smem[];
     float* sk = smem;                        // [C][ldk]
-    float* sv = sk + C * ldk;                // [C][VB]
-    float* sS = sv + C * VB;                 // [K][VB]
+    float* sw = sk + C * ldk;                // [C][VB]: w V
+    float* sS = sw + C * VB;                 // [K][VB]
     float* pw = sS + K * VB;                 // lam^0 .. lam^C
     float* sq = pw + C + 4;                  // [C][ldk]
-    float* sP = sq + C * ldk;                // [C][C + 4]
+    float* sv = sq + C * ldk;                // [C][VB]
+    float* sP = sv + C * VB;                 // [C][ldp]
+    __shared__ float2 lam_full, lam_tail;
+
     const float gd = a.log_decay[g];
+    const int tail = sg.len - (sg.len - 1) / C * C;              // tokens of the last chunk
     if (tid <= C) pw[tid] = (float)pow_decay(gd, tid);
+    if (tid == 96) lam_full = pow2f(gd, C);
+    if (tid == 128) lam_tail = pow2f(gd, sg.len > 0 ? tail : 0);
     if (tid == 0) check_decay(gd);
     const int64_t per_state = (int64_t)a.Hk * V * K, head = ((int64_t)g * V + v0) * K;
     const int64_t ip = a.init ? page_of(a.init_pages, a.npages, sg.seq) : -1;
-    const bool last = sg.j + 1 == sg.n;
     int64_t fp = -1;
-    if (OUT && last && a.fin) {
+    if (OUT && sg.j + 1 == sg.n && a.fin) {
         fp = page_of(a.fin_pages, a.npages, sg.seq);
         if (a.fin_pages && fp >= 0 && page_clash(a, sg.seq, fp, NT)) {
             latch_error(SSD_ERR_INVALID_ARG);
             fp = -1;
         }
     }
-    __syncthreads();
-    // State entering the segment (zero-start without OUT); [V][K] in memory, [K][VB] here.
-    for (int e = tid; e < K * VB; e += NT) {
-        const int kk = e % K, vv = e / K;
-        const int64_t at = head + (int64_t)vv * K + kk;
-        float s = 0.f;
-        if (vv < nv) {
-            if (OUT) {
-                if (sg.j > 0) s = a.slots[(int64_t)(sg.slot0 + sg.j) * per_state + at];
-                else if (ip >= 0) s = sg.n == 1 ? a.init[ip * per_state + at] : a.slots[(int64_t)sg.slot0 * per_state + at];
-            } else if (sg.j == 0 && ip >= 0) {
-                a.slots[(int64_t)sg.slot0 * per_state + at] = a.init[ip * per_state + at];
+    // State entering the segment (zero without OUT); [V][K] in memory, lanes along K.
+    {
+        const float* from = nullptr;
+        if (OUT && sg.j > 0) from = a.slots + (int64_t)(sg.slot0 + sg.j) * per_state + head;
+        else if (OUT && ip >= 0) from = sg.n == 1 ? a.init + ip * per_state + head : a.slots + (int64_t)sg.slot0 * per_state + head;
+        const bool copy = !OUT && sg.j == 0 && ip >= 0;          // for the output pass
+#pragma unroll 4
+        for (int v = warp; v < VB; v += NT / 32)
+            for (int kk = lane; kk < K; kk += 32) {
+                sS[kk * VB + v] = from && v < nv ? from[v * K + kk] : 0.f;
+                if (copy && v < nv)
+                    a.slots[(int64_t)sg.slot0 * per_state + head + v * K + kk] = a.init[ip * per_state + head + v * K + kk];
             }
-        }
-        sS[kk * VB + vv] = s;
     }
 
     const float* kp = static_cast<const float*>(a.k) + sg.start * a.k_stride + (int64_t)g * K;
     const float* vp = static_cast<const float*>(a.v) + sg.start * a.v_stride + (int64_t)g * V + v0;
     const bool need_last = !OUT || fp >= 0;
+    const int tx = tid & 15, ty = tid >> 4;                      // rows ty + 16 i, columns 4 tx ..
     for (int c0 = 0; c0 < sg.len; c0 += C) {
-        const int len = min(C, sg.len - c0);
-        __syncthreads();                     // the last chunk's readers of sk, sv are done
-        for (int e = tid; e < C * (K / 4); e += NT) {
-            const int t = e / (K / 4), c4 = e % (K / 4);
-            const float4 x = t < len ? load4(kp + (int64_t)(c0 + t) * a.k_stride + 4 * c4) : make_float4(0, 0, 0, 0);
-            *reinterpret_cast<float4*>(sk + t * ldk + 4 * c4) = x;
-        }
-        for (int e = tid; e < C * (VB / 4); e += NT) {
-            const int t = e / (VB / 4), c4 = e % (VB / 4);
-            const float4 x = t < len && 4 * c4 < nv ? load4(vp + (int64_t)(c0 + t) * a.v_stride + 4 * c4)
-                                                    : make_float4(0, 0, 0, 0);
-            *reinterpret_cast<float4*>(sv + t * VB + 4 * c4) = x;
-        }
-        if (OUT) {
-            for (int r = 0; r < a.R; ++r) {
-                const float* qp = static_cast<const float*>(a.q) + (sg.start + c0) * a.q_stride + (int64_t)(g * a.R + r) * K;
-                __syncthreads();             // readers of sq, sP are done
-                for (int e = tid; e < C * (K / 4); e += NT) {
-                    const int t = e / (K / 4), c4 = e % (K / 4);
-                    const float4 x = t < len ? load4(qp + (int64_t)t * a.q_stride + 4 * c4) : make_float4(0, 0, 0, 0);
-                    *reinterpret_cast<float4*>(sq + t * ldk + 4 * c4) = x;
-                }
-                __syncthreads();
-                const int tx = tid & 15, ty = tid >> 4;   // rows ty + 16 i, columns tx + 16 j / 4 tx + j
-                {
-                    float acc[4][4] = {};
-                    for (int kk = 0; kk < K; kk += 4) {
-                        float4 x[4], y[4];
+        const int len = min(C, sg.len - c0), end = (len + 3) & ~3;
+        __syncthreads();                     // the last chunk's readers are done (and the tables written)
+        simt_rows<false>(sk, ldk, kp + c0 * a.k_stride, a.k_stride, K, len, nullptr);
+        simt_rows<true>(sw, VB, vp + c0 * a.v_stride, a.v_stride, nv, len, pw);
+        if (OUT) simt_rows<false>(sv, VB, vp + c0 * a.v_stride, a.v_stride, nv, len, nullptr);
+        for (int r = 0; OUT && r < a.R; ++r) {
+            if (r > 0) __syncthreads();      // readers of sq and sP are done
+            simt_rows<false>(sq, ldk, static_cast<const float*>(a.q) + (sg.start + c0) * a.q_stride + (int64_t)(g * a.R + r) * K,
+                             a.q_stride, K, len, nullptr);
+            __syncthreads();
+            {
+                float acc[4][4] = {};        // rows ty + 16 i, source tokens tx + 16 j
+#pragma unroll 2
+                for (int kk = 0; kk < K; kk += 4) {
+                    float4 x[4], y[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            x[i] = *reinterpret_cast<const float4*>(sq + (ty + 16 * i) * ldk + kk);
-                            y[i] = *reinterpret_cast<const float4*>(sk + (tx + 16 * i) * ldk + kk);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                acc[i][j] = fmaf(x[i].x, y[j].x, acc[i][j]);
-                                acc[i][j] = fmaf(x[i].y, y[j].y, acc[i][j]);
-                                acc[i][j] = fmaf(x[i].z, y[j].z, acc[i][j]);
-                                acc[i][j] = fmaf(x[i].w, y[j].w, acc[i][j]);
-                            }
+                    for (int i = 0; i < 4; ++i) {
+                        x[i] = *reinterpret_cast<const float4*>(sq + (ty + 16 * i) * ldk + kk);
+                        y[i] = *reinterpret_cast<const float4*>(sk + (tx + 16 * i) * ldk + kk);
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int t = ty + 16 * i, s = tx + 16 * j;
-                            sP[t * (C + 4) + s] = s <= t ? acc[i][j] * pw[t - s] : 0.f;
+                        for (int j = 0; j <= i; ++j) {            // later blocks lie above the diagonal
+                            acc[i][j] = fmaf(x[i].x, y[j].x, acc[i][j]);
+                            acc[i][j] = fmaf(x[i].y, y[j].y, acc[i][j]);
+                            acc[i][j] = fmaf(x[i].z, y[j].z, acc[i][j]);
+                            acc[i][j] = fmaf(x[i].w, y[j].w, acc[i][j]);
                         }
                 }
-                __syncthreads();
-                float acc[4][4] = {}, inter[4][4] = {};
-                for (int s = 0; s < ty + 49; ++s) {       // sources up to this thread's last row
-                    const float4 y = *reinterpret_cast<const float4*>(sv + s * VB + 4 * tx);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float x = sP[(ty + 16 * i) * (C + 4) + s];
-                        if (s > ty + 16 * i) continue;
-                        acc[i][0] = fmaf(x, y.x, acc[i][0]);
-                        acc[i][1] = fmaf(x, y.y, acc[i][1]);
-                        acc[i][2] = fmaf(x, y.z, acc[i][2]);
-                        acc[i][3] = fmaf(x, y.w, acc[i][3]);
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int t = ty + 16 * i, s = tx + 16 * j;
+                        sP[t * ldp + s] = s <= t ? acc[i][j] * pw[t - s] : 0.f;
                     }
-                }
-                for (int kk = 0; kk < K; ++kk) {
-                    const float4 y = *reinterpret_cast<const float4*>(sS + kk * VB + 4 * tx);
+            }
+            __syncthreads();
+            float4 acc[4], inter[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float x = sq[(ty + 16 * i) * ldk + kk];
-                        inter[i][0] = fmaf(x, y.x, inter[i][0]);
-                        inter[i][1] = fmaf(x, y.y, inter[i][1]);
-                        inter[i][2] = fmaf(x, y.z, inter[i][2]);
-                        inter[i][3] = fmaf(x, y.w, inter[i][3]);
-                    }
-                }
-                float* op = static_cast<float*>(a.o) + ((sg.start + c0) * a.H + g * a.R + r) * (int64_t)V + v0;
+            for (int i = 0; i < 4; ++i) acc[i] = inter[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            simt_tile(acc, sP + ty * ldp, 16 * ldp, sv + 4 * tx, VB, min(end, (ty + 52) & ~3));
+            simt_tile(inter, sq + ty * ldk, 16 * ldk, sS + 4 * tx, VB, K);
+            float* op = static_cast<float*>(a.o) + ((sg.start + c0) * a.H + g * a.R + r) * (int64_t)V + v0 + 4 * tx;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int t = ty + 16 * i;
-                    if (t >= len || 4 * tx >= nv) continue;
-                    const float w = pw[t + 1];
-                    float y[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) y[j] = a.scale * fmaf(w, inter[i][j], acc[i][j]);
-                    *reinterpret_cast<float4*>(op + (int64_t)t * a.H * V + 4 * tx) = make_float4(y[0], y[1], y[2], y[3]);
-                }
+            for (int i = 0; i < 4; ++i) {
+                const int t = ty + 16 * i;
+                if (t >= len || 4 * tx >= nv) continue;
+                const float w = pw[t + 1];
+                *reinterpret_cast<float4*>(op + (int64_t)t * a.H * V) =
+                    make_float4(a.scale * fmaf(w, inter[i].x, acc[i].x), a.scale * fmaf(w, inter[i].y, acc[i].y),
+                                a.scale * fmaf(w, inter[i].z, acc[i].z), a.scale * fmaf(w, inter[i].w, acc[i].w));
             }
         }
         __syncthreads();
         if (c0 + C < sg.len || need_last) {
-            // S = lam^len S + sum_s lam^(len-1-s) k_s v_s^T; rows kk = ty + 16 i, columns 4 tx
-            const float2 lc = pow2f(gd, len);
-            const int tx = tid & 15, ty = tid >> 4;
-            for (int kb = ty; kb < K; kb += 64) {
-                float acc[4][4] = {};
-                for (int s = 0; s < len; ++s) {
-                    const float w = pw[len - 1 - s];
-                    const float4 y = *reinterpret_cast<const float4*>(sv + s * VB + 4 * tx);
+            // S = lam^len S + k^T (w V): rows 4 ty .. of 64, columns 4 tx ..
+            const float2 lam = c0 + C < sg.len ? lam_full : lam_tail;
+            for (int kb = 4 * ty; kb < K; kb += 64) {
+                float4 acc[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float x = kb + 16 * i < K ? w * sk[s * ldk + kb + 16 * i] : 0.f;
-                        acc[i][0] = fmaf(x, y.x, acc[i][0]);
-                        acc[i][1] = fmaf(x, y.y, acc[i][1]);
-                        acc[i][2] = fmaf(x, y.z, acc[i][2]);
-                        acc[i][3] = fmaf(x, y.w, acc[i][3]);
-                    }
+                for (int i = 0; i < 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                for (int s = 0; s < end; ++s) {
+                    const float4 x = *reinterpret_cast<const float4*>(sk + s * ldk + kb);
+                    const float4 y = *reinterpret_cast<const float4*>(sw + s * VB + 4 * tx);
+                    axpy4(acc[0], x.x, y);
+                    axpy4(acc[1], x.y, y);
+                    axpy4(acc[2], x.z, y);
+                    axpy4(acc[3], x.w, y);
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    if (kb + 16 * i >= K) continue;
-                    float* s = sS + (kb + 16 * i) * VB + 4 * tx;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) s[j] = fmaf(lc.x, s[j], fmaf(lc.y, s[j], acc[i][j]));
+                    float4* p = reinterpret_cast<float4*>(sS + (kb + i) * VB + 4 * tx);
+                    float4 s = *p;
+                    s.x = fmaf(lam.x, s.x, fmaf(lam.y, s.x, acc[i].x));
+                    s.y = fmaf(lam.x, s.y, fmaf(lam.y, s.y, acc[i].y));
+                    s.z = fmaf(lam.x, s.z, fmaf(lam.y, s.z, acc[i].z));
+                    s.w = fmaf(lam.x, s.w, fmaf(lam.y, s.w, acc[i].w));
+                    *p = s;
                 }
             }
         }
@@ -354,7 +370,8 @@ __global__ void __launch_bounds__(kSimtThreads) k_la_simt(const __grid_constant_
     __syncthreads();
     float* dst = OUT ? (fp >= 0 ? a.fin + fp * per_state : nullptr) : a.slots + (int64_t)(sg.slot0 + sg.j + 1) * per_state;
     if (dst)
-        for (int e = tid; e < K * nv; e += NT) dst[head + e] = sS[(e % K) * VB + e / K];
+        for (int v = warp; v < nv; v += NT / 32)
+            for (int kk = lane; kk < K; kk += 32) dst[head + v * K + kk] = sS[kk * VB + v];
 }
 
 // ---------------------------------------------------------------------------------

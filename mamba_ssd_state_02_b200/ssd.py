@@ -196,6 +196,8 @@ def _dtype_code(t: torch.Tensor) -> int:
 
 
 def _need(t, name, shape, dtype, device):
+    if t is not None and t.shape == shape and t.dtype is dtype and t.is_cuda and t.device == device and t.is_contiguous():
+        return
     if t is None:
         raise ValueError(f"{name} is required")
     if not t.is_cuda or t.device != device:
@@ -667,19 +669,30 @@ def strict_state_update(cache: ChunkCache, x, dt_raw, dt_bias, A, B, C, D, y=Non
 
 
 # ---------------------------------------------------------------------------------
-# Linear attention with a decay for each head.
+# Linear attention with a decay for each head. A call for one token takes about as long on the
+# host as on the device, so these bindings switch devices only where they have to.
+def _run(dev, fn, *args):
+    if torch.cuda.current_device() == dev.index:
+        status = fn(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, _stream(dev))
+    if status != SSD_OK:
+        _check(status)
+
+
 def _token_stride(t, name, lead, heads, dim, dtype, device):
     """Elements between consecutive tokens of t [*lead, heads, dim], a contiguous tensor or a
     slice of one whose heads are contiguous (lead: (batch, L) or (T,))."""
     shape = (*lead, heads, dim)
+    if t.shape == shape and t.dtype is dtype and t.device == device and t.is_cuda and t.is_contiguous():
+        return heads * dim
     if not t.is_cuda or t.device != device:
         raise ValueError(f"{name} must be on {device}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.is_contiguous():
-        return heads * dim
     st = t.stride()
     if st[-1] != 1 or (heads > 1 and st[-2] != dim):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
@@ -698,14 +711,8 @@ def _pages_arg(pages, name, n, device):
 
 def linear_attn_dims(lead, H, Hk, K, V, dtype_code, nseq=None, strides=(0, 0, 0), n_pages=0, workspace=None):
     """ssd_linear_attn_dims of a dense (lead = (batch, L)) or packed (lead = (T,), nseq) call."""
-    d = SSDLinearAttnDims()
-    if nseq is None:
-        d.batch, d.seqlen = lead
-    else:
-        d.nseq, d.total_tokens = nseq, lead[0]
-    d.nheads, d.nkvheads, d.headdim_k, d.headdim_v = H, Hk, K, V
-    d.q_stride, d.k_stride, d.v_stride = strides
-    d.n_pages, d.dtype = n_pages, dtype_code
+    batch, seqlen, rows = (lead[0], lead[1], 0) if nseq is None else (0, 0, lead[0])
+    d = SSDLinearAttnDims(batch, seqlen, nseq or 0, rows, H, Hk, K, V, *strides, n_pages, dtype_code)
     if workspace is not None:
         d.workspace, d.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     return d
@@ -763,10 +770,9 @@ def linear_attn_fwd(q, k, v, log_decay, scale=None, init_state=None, init_pages=
     else:
         _need(o, "o", (*lead, H, V), dt, dev)
     dims = linear_attn_dims(lead, H, Hk, K, V, _dtype_code(q), nseq if varlen else None, strides, n_pages, workspace)
-    with torch.cuda.device(dev):
-        _check(_lib.ssd_linear_attn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), K ** -0.5 if scale is None else scale,
-                                        _ptr(init_state), _ptr(init_pages), _ptr(cu_seqlens), _ptr(o),
-                                        _ptr(final_state), _ptr(final_pages), ctypes.byref(dims), _stream(dev)))
+    _run(dev, _lib.ssd_linear_attn_fwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+         K ** -0.5 if scale is None else scale, _ptr(init_state), _ptr(init_pages), _ptr(cu_seqlens), o.data_ptr(),
+         final_state.data_ptr(), _ptr(final_pages), ctypes.byref(dims))
     return o, final_state
 
 
@@ -790,10 +796,8 @@ def linear_attn_update(state, q, k, v, log_decay, scale=None, pages=None, o=None
     else:
         _need(o, "o", (b, H, V), dt, dev)
     dims = linear_attn_dims((b, 1), H, Hk, K, V, _dtype_code(q), None, strides, n_pages)
-    with torch.cuda.device(dev):
-        _check(_lib.ssd_linear_attn_update(_ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
-                                           K ** -0.5 if scale is None else scale, _ptr(pages), _ptr(o),
-                                           ctypes.byref(dims), _stream(dev)))
+    _run(dev, _lib.ssd_linear_attn_update, state.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+         K ** -0.5 if scale is None else scale, _ptr(pages), o.data_ptr(), ctypes.byref(dims))
     return o
 
 
@@ -854,8 +858,7 @@ def pages_append(pool: PagePool, rows, copy_last=False):
     """One more (live) page for each listed row, the lowest free ones (ssd_pages_append);
     copy_last: it continues from a copy of the row's last page."""
     n = pool._list(rows, "rows")
-    with torch.cuda.device(pool.device):
-        _check(_lib.ssd_pages_append(pool._ref, rows.data_ptr(), n, 1 if copy_last else 0, _stream(pool.device)))
+    _run(pool.device, _lib.ssd_pages_append, pool._ref, rows.data_ptr(), n, 1 if copy_last else 0)
 
 
 def pages_fork(pool: PagePool, parents, children):
@@ -863,15 +866,13 @@ def pages_fork(pool: PagePool, parents, children):
     (ssd_pages_fork)."""
     n = pool._list(parents, "parents")
     pool._list(children, "children", n)
-    with torch.cuda.device(pool.device):
-        _check(_lib.ssd_pages_fork(pool._ref, parents.data_ptr(), children.data_ptr(), n, _stream(pool.device)))
+    _run(pool.device, _lib.ssd_pages_fork, pool._ref, parents.data_ptr(), children.data_ptr(), n)
 
 
 def pages_free(pool: PagePool, rows):
     """Empties the listed rows; pages that no row holds any more are free (ssd_pages_free)."""
     n = pool._list(rows, "rows")
-    with torch.cuda.device(pool.device):
-        _check(_lib.ssd_pages_free(pool._ref, rows.data_ptr(), n, _stream(pool.device)))
+    _run(pool.device, _lib.ssd_pages_free, pool._ref, rows.data_ptr(), n)
 
 
 def pages_compact(pool: PagePool, remap=None, counts=None):
@@ -882,8 +883,7 @@ def pages_compact(pool: PagePool, remap=None, counts=None):
     counts = torch.empty(2, dtype=torch.int32, device=dev) if counts is None else counts
     _need(remap, "remap", (pool.n_pages,), torch.int32, dev)
     _need(counts, "counts", (2,), torch.int32, dev)
-    with torch.cuda.device(dev):
-        _check(_lib.ssd_pages_compact(pool._ref, remap.data_ptr(), counts.data_ptr(), _stream(dev)))
+    _run(dev, _lib.ssd_pages_compact, pool._ref, remap.data_ptr(), counts.data_ptr())
     return remap, counts
 
 
@@ -891,5 +891,4 @@ def pages_copy(pool: PagePool, src, dst):
     """Copies the bytes of pages src[i] into pages dst[i] in every array (ssd_pages_copy)."""
     n = pool._list(src, "src")
     pool._list(dst, "dst", n)
-    with torch.cuda.device(pool.device):
-        _check(_lib.ssd_pages_copy(pool._ref, src.data_ptr(), dst.data_ptr(), n, _stream(pool.device)))
+    _run(pool.device, _lib.ssd_pages_copy, pool._ref, src.data_ptr(), dst.data_ptr(), n)
