@@ -492,7 +492,8 @@ void ssd_set_segment_tokens(int tokens);
  * flight, and the CTA exits, so the context stays usable; y and the states of that call
  * are undefined. pass = 1 or 2 makes the UMMA warp of every CTA of the segment-state (1)
  * or chunk-scan (2) pass first wait on a barrier that nothing arrives at, so that this
- * wait runs out (each such call takes a few seconds); 0 (or any other value): off.
+ * wait runs out (each such call takes a few seconds); 0 (or any other value): off. The state
+ * and output passes of ssd_linear_attn_fwd (bf16) take 1 and 2 the same way.
  */
 void ssd_test_stall(int pass);
 

@@ -345,9 +345,8 @@ k_la_tc_state(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
 // Output pass. Warp 0 issues the TMA loads; warp 3 the UMMAs of Q K^T, warp 1 those of Oi and
 // Ox, warp 2 those of D (an issuing warp takes its batches in order, and the waits of one
 // product would hold up the others); then three groups of eight warps: scores and w V, outputs,
-// and the state. Q, K and V are double-buffered, and what they have no room for yet is brought
-// into L2. Q K^T runs one unit ahead, in the gap that the outputs leave in the tensor pipe
-// while they are read.
+// and the state. Q, K and V are double-buffered. Q K^T runs one unit ahead, in the gap that the
+// outputs leave in the tensor pipe while they are read.
 //
 // Shared memory: K, V, Q (two buffers each), S (a bf16 pair), w V, and a tile of o on its way
 // out by TMA (a thread's row of o is 64 bytes in another line than its neighbours'; stored from
@@ -435,8 +434,9 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
 
     if (warp == 0) {
         // ------------------------------------------------------------ TMA producer
-        // Per chunk: K, the first Q, V, the other Qs; every load waits until its buffer is free,
-        // and brings the tile two turns of the buffers on into L2.
+        // Per chunk: K, the first Q, V, the other Qs; every load waits until its buffer is free.
+        // (Issuing a 16 KB box takes the thread 320 cycles, five boxes a chunk and head of 128
+        // columns; bringing the next ones into L2 took 100 more each and paid nothing.)
         if (lane == 0 && nt > 0) {
             int c = 0, r = 0, job = 0, n[3] = {0, 0, 0};          // loads of K, V and Q issued
 #pragma unroll 1
@@ -447,18 +447,14 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
                 uint64_t* full = &bars[(k_ ? FULL_K : v_ ? FULL_V : FULL_Q) + b];
                 uint8_t* dst = sm + (k_ ? b * 32768 : v_ ? kOutV + b * 16384 : kOutQ + b * 32768);
                 const int x = v_ ? v0 : 0, head_ = k_ || v_ ? g : g * R + r;
-                const int ahead = k_ || v_ ? c + 2 : R == 1 ? c + 2 : r + 2 < R ? c : c + 1;
-                const int head2 = k_ || v_ || R == 1 ? head_ : r + 2 < R ? head_ + 2 : head_ + 2 - R;
                 if (i >= 2) {
                     wait_bar(full + 2, (i >> 1) - 1, abort_p);    // EMPTY follows FULL
                     if (*abort_p) break;
                 }
                 mbar_arrive_expect_tx(full, tiles * 16384);
 #pragma unroll 1
-                for (int t = 0; t < tiles; ++t) {
+                for (int t = 0; t < tiles; ++t)
                     tma_load_3d(dst + t * 16384, map, full, x + 64 * t, head_, (int)(sg.start + (int64_t)c * kTcC));
-                    if (ahead < nt) tma_prefetch_3d(map, x + 64 * t, head2, (int)(sg.start + (int64_t)ahead * kTcC));
-                }
                 if (k_) ++n[0]; else if (v_) ++n[1]; else { ++n[2]; ++r; }
                 if (++job == R + 2) {
                     job = r = 0;
@@ -615,7 +611,7 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[W_READY]);
         };
-        int u = 0, w_next = 0;               // unit; chunk whose w V is written next
+        int u = 0;
 #pragma unroll 1
         for (int c = 0; c < nt; ++c) {
             const int nb = blocks_of(c);
@@ -632,6 +628,8 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
 #pragma unroll 1
             for (int r = 0; r < R; ++r, ++u) {
                 const uint32_t tP = tbase + 128 * (u & 1) + lanes;
+                // w V first: K's buffer is free only once it has met it
+                if (r == 0 && c + 1 < nt) write_w(c);
                 wait_bar(&bars[QK_DONE + (u & 1)], u >> 1, abort_p);
                 tc_fence_after();
 #pragma unroll 1
@@ -674,10 +672,6 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[P_READY + (u & 1)]);
-                // w V of the first chunk, and of the next one once the last unit's scores are on
-                // their way (its V may be loaded behind the Q of this chunk's units).
-                const int upto = min(nt - 2, r == R - 1 ? c + 1 : c);
-                while (w_next <= upto) write_w(w_next++);
             }
         }
     } else if (warp < 4 + kScoreWarps + kOutWarps) {

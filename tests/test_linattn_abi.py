@@ -81,17 +81,20 @@ def test_small_or_misaligned_workspace(ssd):
     assert _fwd(ssd, d, cu=P) == ssd.SSD_ERR_INVALID_ARG
 
 
-def test_workspace_holds_a_state_per_segment(ssd):
-    one = ssd.linear_attn_workspace_size(_dims(ssd, lead=(64, 512), H=64, Hk=64))
+def test_workspace_holds_the_states_of_the_segments(ssd):
+    state = 64 * 64 * 64 * 4                            # 64 heads of [64][64] floats
+    f32 = dict(H=64, Hk=64, dtype_code=ssd.SSD_DTYPE_F32)
+    # fp32, 64 sequences: CTAs for every SM without cutting a sequence, so nothing but the four
+    # 256-byte pieces of a packed call without sequences
+    assert ssd.linear_attn_workspace_size(_dims(ssd, lead=(64, 512), **f32)) == 4 * 256
+    # bf16: a state per segment and one per sequence
+    assert ssd.linear_attn_workspace_size(_dims(ssd, lead=(64, 512), H=64, Hk=64)) == 64 * 2 * state
     ssd.set_segment_tokens(128)
     try:
-        many = ssd.linear_attn_workspace_size(_dims(ssd, lead=(64, 512), H=64, Hk=64))
+        for kw in (f32, dict(H=64, Hk=64)):
+            assert ssd.linear_attn_workspace_size(_dims(ssd, lead=(64, 512), **kw)) == 64 * 5 * state
     finally:
         ssd.set_segment_tokens(0)
-    # a CTA for every SM without cutting a sequence: nothing for the dense call, and the four
-    # 256-byte pieces of a packed call without sequences
-    assert one == 4 * 256
-    assert many >= 64 * 4 * 64 * 64 * 64 * 4
 
 
 def _pool(ssd, **kw):

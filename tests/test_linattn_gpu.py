@@ -486,3 +486,26 @@ def test_refusals_of_the_binding(ssd, cuda_dev):
         with pytest.raises(ssd.SSDError, match="UNSUPPORTED"):
             ssd.linear_attn_fwd(z(K), z(K), z(V), d["ld"], cu_seqlens=cu_of([4], cuda_dev))
     ssd.device_status()
+
+
+@pytest.mark.parametrize("stalled_pass", [1, 2])
+def test_wait_runs_out_and_context_stays_usable(ssd, cuda_dev, stalled_pass):
+    """The test hook makes one pass's UMMA warp wait for a barrier that nothing arrives at: the
+    bounded waits end the call, SSD_ERR_TIMEOUT is latched and the next call is right."""
+    lens, H, K, V = [300, 40], 2, 64, 64
+    d = make(cuda_dev, lens, torch.bfloat16, H, H, K, V, seed=14)
+    cu = cu_of(lens, cuda_dev)
+    ssd.device_status()
+    ssd.test_stall(stalled_pass)
+    try:
+        ssd.linear_attn_fwd(d["q"], d["k"], d["v"], d["ld"], init_state=d["s0"], cu_seqlens=cu)
+        torch.cuda.synchronize()
+        with pytest.raises(ssd.SSDError, match="TIMEOUT"):
+            ssd.device_status()
+    finally:
+        ssd.test_stall(0)
+    ssd.device_status()
+    o, fin = ssd.linear_attn_fwd(d["q"], d["k"], d["v"], d["ld"], init_state=d["s0"], cu_seqlens=cu)
+    ssd.device_status()
+    ref = LO.linattn(d["q"], d["k"], d["v"], d["ld"], K ** -0.5, d["s0"], lens)
+    check(o, fin, ref, torch.bfloat16, K, 300)
