@@ -362,7 +362,7 @@ ssd_status ssd_linear_attn_fwd_workspace_size(const ssd_linear_attn_dims* dims, 
  *   final_state: output, the states after each sequence's last token (the initial state
  *     for an empty sequence), or NULL; final_pages: page list for it, or NULL.
  *   init_state and final_state may be the same array (states continue in place); they must
- *   not overlap otherwise. With a page list, a final page that an earlier sequence writes,
+ *   not overlap otherwise, and o overlaps nothing. With a page list, a final page that an earlier sequence writes,
  *   or that another sequence starts from (one array), is not written and latches
  *   SSD_ERR_INVALID_ARG. With page lists both arrays have n_pages states.
  *   scale: usually 1 / sqrt(K).

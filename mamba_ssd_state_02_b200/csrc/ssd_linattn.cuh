@@ -103,6 +103,7 @@ __device__ __noinline__ int64_t page_of(const int32_t* pages, int64_t npages, in
 __device__ __noinline__ bool page_clash(const Args& a, int32_t s, int64_t p, int threads) {
     int bad = 0;
     const bool one_pool = a.init == a.fin;
+    if (!a.fin_pages && !(a.init_pages && one_pool)) return false;
     for (int32_t i = threadIdx.x; i < a.nseq; i += threads) {
         if (i == s) continue;
         if (i < s && a.fin_pages && a.fin_pages[i] == p) bad = 1;
@@ -257,7 +258,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) k_la_simt(const __grid_consta
     int64_t fp = -1;
     if (OUT && sg.j + 1 == sg.n && a.fin) {
         fp = page_of(a.fin_pages, a.npages, sg.seq);
-        if (a.fin_pages && fp >= 0 && page_clash(a, sg.seq, fp, NT)) {
+        if (fp >= 0 && page_clash(a, sg.seq, fp, NT)) {
             latch_error(SSD_ERR_INVALID_ARG);
             fp = -1;
         }

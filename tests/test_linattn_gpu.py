@@ -3,9 +3,11 @@ recurrence, element by element.
 
 Tolerances, with u = 2^-8 (bf16) or 2^-24 (fp32) half a step of the type:
 * o is rounded once to its type: u |o|.
-* bf16: the masked scores lam^(t-s) q.k are rounded to bf16 before they meet v: u * o_score.
-  The state enters that product as a bf16 pair, an error of at most u^2 = 2^-16 of it: part of
-  o_mag. An element bound of u |o| + u o_score + 2^-16 o_mag + (fp32 sums below).
+* bf16: a source token of the same chunk reaches o through its masked score lam^(t-s) q.k,
+  rounded to bf16 once; an earlier one through lam^.. v, rounded to bf16 once on its way into
+  the state: u * o_score for both. The state enters its product with q as a bf16 pair, an error
+  of at most u^2 = 2^-16 of it: part of o_mag. An element bound of u |o| + u o_score + 2^-16
+  o_mag + (fp32 sums below).
 * fp32 sums: dot products over K <= 128, chunk sums over at most 128 tokens and one more sum
   per chunk, the powers of lam rounded once (2^-24) and one product each: with n = K + 128 +
   128 + 8 * chunks roundings of at most 2^-23 each (the tensor cores may truncate, a whole step
@@ -265,6 +267,23 @@ def test_clashing_pages_are_refused(ssd, cuda_dev, ip, fp, kept, seg):
     assert torch.equal(pool[:3], d["s0"]) and bool((pool[5] == 7.0).all())
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_states_that_change_places_in_one_array_are_refused(ssd, cuda_dev, dtype):
+    """Sequence 0 would start from state 1 and end in state 0, sequence 1 the other way round."""
+    lens, H, K, V = [40, 60, 20], 2, 64, 64
+    d = make(cuda_dev, lens, dtype, H, H, K, V, seed=15)
+    swap = torch.tensor([1, 0, 2], dtype=torch.int32, device=cuda_dev)
+    ref = LO.linattn(d["q"], d["k"], d["v"], d["ld"], K ** -0.5, d["s0"][swap.long()], lens)
+    s = d["s0"].clone()
+    ssd.device_status()
+    o, _ = ssd.linear_attn_fwd(d["q"], d["k"], d["v"], d["ld"], init_state=s, init_pages=swap, cu_seqlens=cu_of(lens, cuda_dev),
+                               final_state=s)
+    with pytest.raises(ssd.SSDError, match="INVALID_ARG"):
+        ssd.device_status()
+    assert torch.equal(s[:2], d["s0"][:2])
+    check(o, torch.cat([ref["final"][:2].float(), s[2:]]), ref, dtype, K, 60)
+
+
 def test_device_errors(ssd, cuda_dev):
     lens, H, K, V = [40, 24], 2, 64, 64
     d = make(cuda_dev, lens, torch.float32, H, H, K, V)
@@ -373,6 +392,30 @@ def test_a_page_named_twice_and_pages_out_of_range(ssd, cuda_dev):
         ssd.device_status()
     assert torch.equal(o[0], want[0]) and bool((o[1:] == 5.0).all())
     assert torch.equal(pool, one) and torch.equal(pool[[0, 1, 3]], before[[0, 1, 3]])
+
+
+def test_offsets_past_32_bits(ssd, cuda_dev):
+    """A pool of 2^31 state elements and more: single tokens and prompts on its last pages."""
+    H, K, V, n = 64, 128, 128, 2100                  # 4 MiB a page, 8.8 GB
+    lens = [1, 130]
+    d = make(cuda_dev, lens, torch.bfloat16, H, H, K, V, seed=16, decay=-0.1)
+    pool = torch.empty(n, H, V, K, device=cuda_dev)
+    assert pool.numel() > 1 << 31
+    pages = torch.tensor([n - 1, n - 2], dtype=torch.int32, device=cuda_dev)
+    pool[pages.long()] = d["s0"]
+    one = [d[x][:2].contiguous() for x in "qkv"]
+    ref = LO.linattn(*one, d["ld"], K ** -0.5, d["s0"], [1, 1])
+    o = ssd.linear_attn_update(pool, *one, d["ld"], pages=pages)
+    ssd.device_status()
+    tol = 2.0 ** -8 * ref["o"].abs() + (K + 8) * 2.0 ** -24 * ref["o_mag"]
+    assert bool(((o.double() - ref["o"]).abs() <= tol).all())
+    assert bool(((pool[pages.long()].double() - ref["final"]).abs() <= 8 * 2.0 ** -24 * ref["s_mag"]).all())
+    pool[pages.long()] = d["s0"]
+    ref = LO.linattn(d["q"], d["k"], d["v"], d["ld"], K ** -0.5, d["s0"], lens)
+    o, _ = ssd.linear_attn_fwd(d["q"], d["k"], d["v"], d["ld"], init_state=pool, init_pages=pages, cu_seqlens=cu_of(lens, cuda_dev),
+                               final_state=pool, final_pages=pages)
+    ssd.device_status()
+    check(o, pool[pages.long()], ref, torch.bfloat16, K, 130)
 
 
 # --------------------------------------------------------------------------------- together
