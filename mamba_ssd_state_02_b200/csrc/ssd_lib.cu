@@ -1357,7 +1357,8 @@ int la_segment_tokens(const LaPlan& p) {
     int64_t ls = 2;
     for (int64_t m = 2; m <= 8192; m *= 2) {
         const double longest = std::min<double>((double)m, 2 * mean), cost = a.R + 0.6;
-        const double c = U * cost + 0.5 * longest * cost + (start + state_start) * U / std::min<double>((double)m, mean);
+        double c = U * cost + 0.5 * longest * cost + (start + state_start) * U / std::min<double>((double)m, mean);
+        if (m * kC < p.T) c += p.bf16 ? 3 : 2;                    // the passing kernel (and an fp32 state pass)
         if (m == 2 || c < best) {
             best = c;
             ls = m;
@@ -1448,8 +1449,23 @@ ssd_status la_plan(const ssd_linear_attn_dims* d, bool varlen, LaPlan* out) {
 }
 
 // One pass over `segs` segments: the state each adds (OUT false), or the outputs.
+struct LaMaps {
+    CUtensorMap q{}, k{}, v{}, o{};
+};
+
+bool la_maps(const LaPlan& p, LaMaps* m) {
+    const la::Args& a = p.a;
+    const uint64_t T = (uint64_t)p.T;
+    if (T == 0) return true;
+    auto map = [&](CUtensorMap* to, const void* base, int dim, int heads, int64_t stride) {
+        return make_map3(to, base, dim, heads, T, (uint64_t)dim * 2, (uint64_t)stride * 2, 64, 1, la::kTcC);
+    };
+    return map(&m->q, a.q, a.K, a.H, a.q_stride) && map(&m->k, a.k, a.K, a.Hk, a.k_stride) &&
+           map(&m->v, a.v, a.V, a.Hk, a.v_stride) && map(&m->o, a.o, a.V, a.H, (int64_t)a.H * a.V);
+}
+
 template <bool OUT>
-ssd_status launch_la(const LaPlan& p, int64_t segs, cudaStream_t st) {
+ssd_status launch_la(const LaPlan& p, const LaMaps& m, int64_t segs, cudaStream_t st) {
     const la::Args& a = p.a;
     const unsigned grid = (unsigned)(segs * a.Hk * ((a.V + 63) / 64));
     static_assert(la::kSimtV == 64 && la::kTcV == 64, "both kernels take 64 columns of V per CTA");
@@ -1461,25 +1477,18 @@ ssd_status launch_la(const LaPlan& p, int64_t segs, cudaStream_t st) {
         la::k_la_simt<OUT><<<grid, la::kSimtThreads, smem, st>>>(a);
         return SSD_OK;
     }
-    CUtensorMap mq{}, mk{}, mv{}, mo{};
-    const uint64_t T = (uint64_t)p.T;
-    if (T > 0 && ((OUT && !make_map3(&mq, a.q, a.K, a.H, T, (uint64_t)a.K * 2, (uint64_t)a.q_stride * 2, 64, 1, la::kTcC)) ||
-                  (OUT && !make_map3(&mo, a.o, a.V, a.H, T, (uint64_t)a.V * 2, (uint64_t)a.H * a.V * 2, 64, 1, la::kTcC)) ||
-                  !make_map3(&mk, a.k, a.K, a.Hk, T, (uint64_t)a.K * 2, (uint64_t)a.k_stride * 2, 64, 1, la::kTcC) ||
-                  !make_map3(&mv, a.v, a.V, a.Hk, T, (uint64_t)a.V * 2, (uint64_t)a.v_stride * 2, 64, 1, la::kTcC)))
-        return fail(SSD_ERR_CUDA, "cuTensorMapEncodeTiled failed (q/k/v/o tensor maps)");
     la::Args b = a;
     b.stall = g_test_stall.load() == (OUT ? 2 : 1);
     if (OUT) {
         cudaError_t e = cudaFuncSetAttribute(la::k_la_tc_out, cudaFuncAttributeMaxDynamicSharedMemorySize, la::kOutSmem);
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(linear attention)");
         StageScope sc(ST_LA_SCAN, st);
-        la::k_la_tc_out<<<grid, la::kOutThreads, la::kOutSmem, st>>>(mq, mk, mv, mo, b);
+        la::k_la_tc_out<<<grid, la::kOutThreads, la::kOutSmem, st>>>(m.q, m.k, m.v, m.o, b);
     } else {
         cudaError_t e = cudaFuncSetAttribute(la::k_la_tc_state, cudaFuncAttributeMaxDynamicSharedMemorySize, la::kStateSmem);
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(linear attention)");
         StageScope sc(ST_LA_STATE, st);
-        la::k_la_tc_state<<<grid, la::kStateThreads, la::kStateSmem, st>>>(mk, mv, b);
+        la::k_la_tc_state<<<grid, la::kStateThreads, la::kStateSmem, st>>>(m.k, m.v, b);
     }
     return SSD_OK;
 }
@@ -1567,7 +1576,9 @@ extern "C" ssd_status ssd_linear_attn_fwd(const void* q, const void* k, const vo
     a.slots = reinterpret_cast<float*>(ws + p.off_slots);
     a.two_pass = two_pass;
     int n = 0;
-    if (cu_seqlens) {
+    LaMaps maps;
+    if (p.bf16 && !la_maps(p, &maps)) s = fail(SSD_ERR_CUDA, "cuTensorMapEncodeTiled failed (q/k/v/o tensor maps)");
+    if (s == SSD_OK && cu_seqlens) {
         auto* table = reinterpret_cast<ChunkEntry*>(ws + p.off_table);
         auto* first = reinterpret_cast<int32_t*>(ws + p.off_first);
         auto* count = reinterpret_cast<int32_t*>(ws + p.off_count);
@@ -1581,9 +1592,9 @@ extern "C" ssd_status ssd_linear_attn_fwd(const void* q, const void* k, const vo
                                                    nullptr, nullptr, true);
         ++n;
     }
-    if (two_pass) {
+    if (s == SSD_OK && two_pass) {
         const int64_t segs = cu_seqlens || p.bf16 ? p.max_segs : (int64_t)a.nseq * (a.nps - 1);
-        s = launch_la<false>(p, segs, st);
+        s = launch_la<false>(p, maps, segs, st);
         ++n;
     }
     if (s == SSD_OK && many) {
@@ -1593,7 +1604,7 @@ extern "C" ssd_status ssd_linear_attn_fwd(const void* q, const void* k, const vo
         ++n;
     }
     if (s == SSD_OK) {
-        s = launch_la<true>(p, p.max_segs, st);
+        s = launch_la<true>(p, maps, p.max_segs, st);
         ++n;
     }
     cudaError_t e = cudaGetLastError();
