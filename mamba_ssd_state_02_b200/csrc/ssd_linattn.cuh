@@ -179,24 +179,31 @@ constexpr int kSimtThreads = 256;
 
 __host__ __device__ constexpr int simt_ld(int n) { return n + 4; }   // row stride: rows start in other banks
 __host__ __device__ constexpr size_t simt_smem(int K, bool out) {
-    return sizeof(float) * ((size_t)kSimtC * simt_ld(K) + kSimtC * kSimtV + (size_t)K * kSimtV + kSimtC + 4 +
+    return sizeof(float) * ((size_t)kSimtC * simt_ld(K) + kSimtC * kSimtV + (size_t)K * simt_ld(kSimtV) + kSimtC + 4 +
                             (out ? (size_t)kSimtC * simt_ld(K) + kSimtC * kSimtV + kSimtC * simt_ld(kSimtC) : 0));
 }
 
-// Rows [0, 64) of a [tokens][n] matrix (n a multiple of 8, `stride` elements between rows) into
-// shared memory with row stride ld; rows from len on are zeros. SCALE: row s times f[len-1-s].
-template <bool SCALE>
-__device__ __forceinline__ void simt_rows(float* dst, int ld, const float* src, int64_t stride, int n, int len, const float* f) {
+// Rows [0, 64) of a [tokens][n] matrix (n a multiple of 8, `stride` elements between rows) on
+// their way into shared memory with row stride ld (asynchronous copies: all of a chunk's are in
+// flight at once); rows from len on are zeros.
+__device__ __forceinline__ void simt_rows(float* dst, int ld, const float* src, int64_t stride, int n, int len) {
     const int per = n / 4;
     for (int e = threadIdx.x; e < kSimtC * per; e += kSimtThreads) {
         const int t = e / per, c4 = e - t * per;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (t < len) x = *reinterpret_cast<const float4*>(src + t * stride + 4 * c4);
-        if (SCALE) {
-            const float w = t < len ? f[len - 1 - t] : 0.f;
-            x = make_float4(w * x.x, w * x.y, w * x.z, w * x.w);
-        }
-        *reinterpret_cast<float4*>(dst + t * ld + 4 * c4) = x;
+        float* to = dst + t * ld + 4 * c4;
+        if (t < len) cp_async16(to, src + t * stride + 4 * c4);
+        else *reinterpret_cast<float4*>(to) = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+}
+
+// dst row s = f[len-1-s] times row s of src, the elements that the thread has copied itself.
+__device__ __forceinline__ void simt_scale(float* dst, const float* src, int ld, int n, int len, const float* f) {
+    const int per = n / 4;
+    for (int e = threadIdx.x; e < kSimtC * per; e += kSimtThreads) {
+        const int t = e / per, at = t * ld + 4 * (e - t * per);
+        const float w = t < len ? f[len - 1 - t] : 0.f;
+        const float4 x = *reinterpret_cast<const float4*>(src + at);
+        *reinterpret_cast<float4*>(dst + at) = make_float4(w * x.x, w * x.y, w * x.z, w * x.w);
     }
 }
 
@@ -229,7 +236,7 @@ __device__ __forceinline__ void simt_tile(float4 (&acc)[4], const float* x, int 
 
 template <bool OUT>
 __global__ void __launch_bounds__(kSimtThreads, 2) k_la_simt(const __grid_constant__ Args a) {
-    constexpr int C = kSimtC, VB = kSimtV, NT = kSimtThreads, ldp = simt_ld(C);
+    constexpr int C = kSimtC, VB = kSimtV, NT = kSimtThreads, ldp = simt_ld(C), lds = simt_ld(VB);
     const int nvb = (a.V + VB - 1) / VB;
     const int vb = blockIdx.x % nvb, g = (blockIdx.x / nvb) % a.Hk;
     Seg sg;
@@ -240,8 +247,8 @@ __global__ void __launch_bounds__(kSimtThreads, 2) k_la_simt(const __grid_consta
     extern __shared__ __align__(16) float smem[];
     float* sk = smem;                        // [C][ldk]
     float* sw = sk + C * ldk;                // [C][VB]: w V
-    float* sS = sw + C * VB;                 // [K][VB]
-    float* pw = sS + K * VB;                 // lam^0 .. lam^C
+    float* sS = sw + C * VB;                 // [K][lds]
+    float* pw = sS + K * lds;                // lam^0 .. lam^C
     float* sq = pw + C + 4;                  // [C][ldk]
     float* sv = sq + C * ldk;                // [C][VB]
     float* sP = sv + C * VB;                 // [C][ldp]
@@ -272,7 +279,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) k_la_simt(const __grid_consta
 #pragma unroll 4
         for (int v = warp; v < VB; v += NT / 32)
             for (int kk = lane; kk < K; kk += 32) {
-                sS[kk * VB + v] = from && v < nv ? from[v * K + kk] : 0.f;
+                sS[kk * lds + v] = from && v < nv ? from[v * K + kk] : 0.f;
                 if (copy && v < nv)
                     a.slots[(int64_t)sg.slot0 * per_state + head + v * K + kk] = a.init[ip * per_state + head + v * K + kk];
             }
@@ -285,14 +292,25 @@ __global__ void __launch_bounds__(kSimtThreads, 2) k_la_simt(const __grid_consta
     for (int c0 = 0; c0 < sg.len; c0 += C) {
         const int len = min(C, sg.len - c0), end = (len + 3) & ~3;
         __syncthreads();                     // the last chunk's readers are done (and the tables written)
-        simt_rows<false>(sk, ldk, kp + c0 * a.k_stride, a.k_stride, K, len, nullptr);
-        simt_rows<true>(sw, VB, vp + c0 * a.v_stride, a.v_stride, nv, len, pw);
-        if (OUT) simt_rows<false>(sv, VB, vp + c0 * a.v_stride, a.v_stride, nv, len, nullptr);
+        auto rows_q = [&](int r) {
+            simt_rows(sq, ldk, static_cast<const float*>(a.q) + (sg.start + c0) * a.q_stride + (int64_t)(g * a.R + r) * K,
+                      a.q_stride, K, len);
+        };
+        simt_rows(sk, ldk, kp + c0 * a.k_stride, a.k_stride, K, len);
+        simt_rows(OUT ? sv : sw, VB, vp + c0 * a.v_stride, a.v_stride, nv, len);
+        if (OUT) rows_q(0);
+        cp_async_commit();
+        cp_async_wait<0>();
+        simt_scale(sw, OUT ? sv : sw, VB, nv, len, pw);
+        __syncthreads();
         for (int r = 0; OUT && r < a.R; ++r) {
-            if (r > 0) __syncthreads();      // readers of sq and sP are done
-            simt_rows<false>(sq, ldk, static_cast<const float*>(a.q) + (sg.start + c0) * a.q_stride + (int64_t)(g * a.R + r) * K,
-                             a.q_stride, K, len, nullptr);
-            __syncthreads();
+            if (r > 0) {
+                __syncthreads();             // readers of sq and sP are done
+                rows_q(r);
+                cp_async_commit();
+                cp_async_wait<0>();
+                __syncthreads();
+            }
             {
                 float acc[4][4] = {};        // rows ty + 16 i, source tokens tx + 16 j
 #pragma unroll 2
@@ -326,7 +344,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) k_la_simt(const __grid_consta
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[i] = inter[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             simt_tile(acc, sP + ty * ldp, 16 * ldp, sv + 4 * tx, VB, min(end, (ty + 52) & ~3));
-            simt_tile(inter, sq + ty * ldk, 16 * ldk, sS + 4 * tx, VB, K);
+            simt_tile(inter, sq + ty * ldk, 16 * ldk, sS + 4 * tx, lds, K);
             float* op = static_cast<float*>(a.o) + ((sg.start + c0) * a.H + g * a.R + r) * (int64_t)V + v0 + 4 * tx;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -338,7 +356,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) k_la_simt(const __grid_consta
                                 a.scale * fmaf(w, inter[i].z, acc[i].z), a.scale * fmaf(w, inter[i].w, acc[i].w));
             }
         }
-        __syncthreads();
+        if (OUT) __syncthreads();            // readers of the state are done
         if (c0 + C < sg.len || need_last) {
             // S = lam^len S + k^T (w V): rows 4 ty .. of 64, columns 4 tx ..
             const float2 lam = c0 + C < sg.len ? lam_full : lam_tail;
@@ -357,7 +375,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) k_la_simt(const __grid_consta
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    float4* p = reinterpret_cast<float4*>(sS + (kb + i) * VB + 4 * tx);
+                    float4* p = reinterpret_cast<float4*>(sS + (kb + i) * lds + 4 * tx);
                     float4 s = *p;
                     s.x = fmaf(lam.x, s.x, fmaf(lam.y, s.x, acc[i].x));
                     s.y = fmaf(lam.x, s.y, fmaf(lam.y, s.y, acc[i].y));
@@ -372,7 +390,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) k_la_simt(const __grid_consta
     float* dst = OUT ? (fp >= 0 ? a.fin + fp * per_state : nullptr) : a.slots + (int64_t)(sg.slot0 + sg.j + 1) * per_state;
     if (dst)
         for (int v = warp; v < nv; v += NT / 32)
-            for (int kk = lane; kk < K; kk += 32) dst[head + v * K + kk] = sS[kk * VB + v];
+            for (int kk = lane; kk < K; kk += 32) dst[head + v * K + kk] = sS[kk * lds + v];
 }
 
 // ---------------------------------------------------------------------------------
