@@ -183,28 +183,33 @@ __host__ __device__ constexpr size_t simt_smem(int K, bool out) {
                             (out ? (size_t)kSimtC * simt_ld(K) + kSimtC * kSimtV + kSimtC * simt_ld(kSimtC) : 0));
 }
 
-// Rows [0, 64) of a [tokens][n] matrix (n a multiple of 8, `stride` elements between rows) on
-// their way into shared memory with row stride ld (asynchronous copies: all of a chunk's are in
-// flight at once); rows from len on are zeros.
+// The 16-byte pieces of a chunk's [64][n] rows as the threads share them out (n a multiple of 8):
+// a power of two of lanes per row, f(row, first column).
+template <typename F>
+__device__ __forceinline__ void simt_share(int n, F f) {
+    const int bits = 32 - __clz(n / 4 - 1), c = 4 * (threadIdx.x & ((1 << bits) - 1));
+    if (c >= n) return;
+#pragma unroll 1
+    for (int t = threadIdx.x >> bits; t < kSimtC; t += kSimtThreads >> bits) f(t, c);
+}
+
+// Rows of a [tokens][n] matrix (`stride` elements between rows) on their way into shared memory
+// with row stride ld (asynchronous copies: all of a chunk's are in flight at once); rows from
+// len on are zeros.
 __device__ __forceinline__ void simt_rows(float* dst, int ld, const float* src, int64_t stride, int n, int len) {
-    const int per = n / 4;
-    for (int e = threadIdx.x; e < kSimtC * per; e += kSimtThreads) {
-        const int t = e / per, c4 = e - t * per;
-        float* to = dst + t * ld + 4 * c4;
-        if (t < len) cp_async16(to, src + t * stride + 4 * c4);
-        else *reinterpret_cast<float4*>(to) = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
+    simt_share(n, [&](int t, int c) {
+        if (t < len) cp_async16(dst + t * ld + c, src + t * stride + c);
+        else *reinterpret_cast<float4*>(dst + t * ld + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+    });
 }
 
 // dst row s = f[len-1-s] times row s of src, the elements that the thread has copied itself.
 __device__ __forceinline__ void simt_scale(float* dst, const float* src, int ld, int n, int len, const float* f) {
-    const int per = n / 4;
-    for (int e = threadIdx.x; e < kSimtC * per; e += kSimtThreads) {
-        const int t = e / per, at = t * ld + 4 * (e - t * per);
+    simt_share(n, [&](int t, int c) {
         const float w = t < len ? f[len - 1 - t] : 0.f;
-        const float4 x = *reinterpret_cast<const float4*>(src + at);
-        *reinterpret_cast<float4*>(dst + at) = make_float4(w * x.x, w * x.y, w * x.z, w * x.w);
-    }
+        const float4 x = *reinterpret_cast<const float4*>(src + t * ld + c);
+        *reinterpret_cast<float4*>(dst + t * ld + c) = make_float4(w * x.x, w * x.y, w * x.z, w * x.w);
+    });
 }
 
 __device__ __forceinline__ void axpy4(float4& acc, float x, const float4& y) {
@@ -289,6 +294,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) k_la_simt(const __grid_consta
     const float* vp = static_cast<const float*>(a.v) + sg.start * a.v_stride + (int64_t)g * V + v0;
     const bool need_last = !OUT || fp >= 0;
     const int tx = tid & 15, ty = tid >> 4;                      // rows ty + 16 i, columns 4 tx ..
+#pragma unroll 1
     for (int c0 = 0; c0 < sg.len; c0 += C) {
         const int len = min(C, sg.len - c0), end = (len + 3) & ~3;
         __syncthreads();                     // the last chunk's readers are done (and the tables written)
@@ -303,6 +309,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) k_la_simt(const __grid_consta
         cp_async_wait<0>();
         simt_scale(sw, OUT ? sv : sw, VB, nv, len, pw);
         __syncthreads();
+#pragma unroll 1
         for (int r = 0; OUT && r < a.R; ++r) {
             if (r > 0) {
                 __syncthreads();             // readers of sq and sP are done
@@ -360,6 +367,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) k_la_simt(const __grid_consta
         if (c0 + C < sg.len || need_last) {
             // S = lam^len S + k^T (w V): rows 4 ty .. of 64, columns 4 tx ..
             const float2 lam = c0 + C < sg.len ? lam_full : lam_tail;
+#pragma unroll 1
             for (int kb = 4 * ty; kb < K; kb += 64) {
                 float4 acc[4];
 #pragma unroll
