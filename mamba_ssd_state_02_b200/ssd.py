@@ -17,6 +17,7 @@ Functions mirror the C entry points:
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -771,10 +772,14 @@ def linear_attn_fwd(q, k, v, log_decay, scale=None, init_state=None, init_pages=
     else:
         _need(o, "o", (*lead, H, V), dt, dev)
     dims = linear_attn_dims(lead, H, Hk, K, V, _dtype_code(q), nseq if varlen else None, strides, n_pages, workspace)
-    if workspace is None:
+    if workspace is not None:
+        if not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    else:
         # From torch's cache: the library's own stream-ordered allocation gives its memory back at
         # every synchronization, and mapping it again took 0.5 ms of a call that runs for 0.28 ms.
-        need = linear_attn_workspace_size(dims)
+        with contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev):
+            need = linear_attn_workspace_size(dims)       # the planner asks the device for its SMs
         if need > 256:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
             dims.workspace, dims.workspace_bytes = workspace.data_ptr(), need

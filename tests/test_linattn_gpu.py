@@ -506,6 +506,30 @@ def test_captured_and_replayed(ssd, cuda_dev):
     ssd.device_status()
 
 
+def test_two_captured_prompts_replay_at_once(ssd, cuda_dev):
+    """Two graphs, each with a scratch of its own, replayed side by side on two streams."""
+    lens, H, K, V = [900, 30, 700], 4, 64, 64
+    cu, calls = cu_of(lens, cuda_dev), []
+    for seed in (31, 32):
+        d = make(cuda_dev, lens, torch.bfloat16, H, H, K, V, seed=seed)
+        ref = LO.linattn(d["q"], d["k"], d["v"], d["ld"], K ** -0.5, d["s0"], lens)
+        run = lambda d=d: ssd.linear_attn_fwd(d["q"], d["k"], d["v"], d["ld"], init_state=d["s0"], cu_seqlens=cu)  # noqa: E731
+        run()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = run()
+        calls.append((torch.cuda.Stream(), graph, out, ref, d))       # the graph reads d again
+    for _ in range(3):
+        for st, graph, *_ in calls:
+            with torch.cuda.stream(st):
+                graph.replay()
+    torch.cuda.synchronize()
+    ssd.device_status()
+    for _st, _graph, (o, fin), ref, _d in calls:
+        check(o, fin, ref, torch.bfloat16, K, 900)
+
+
 def test_refusals_of_the_binding(ssd, cuda_dev):
     d = make(cuda_dev, [32], torch.bfloat16, 4, 2, 64, 64)
     cu = cu_of([32], cuda_dev)
@@ -519,6 +543,8 @@ def test_refusals_of_the_binding(ssd, cuda_dev):
                     (dict(o=torch.empty(32, 4, 32, dtype=torch.bfloat16, device=cuda_dev)), ValueError)]:
         with pytest.raises(err):
             call(**kw)
+    with pytest.raises(ValueError, match="workspace"):
+        call(workspace=torch.empty(1 << 20, dtype=torch.uint8))
     off = torch.empty(32 * 4 * 64 + 1, dtype=torch.bfloat16, device=cuda_dev)[1:].view(32, 4, 64)
     with pytest.raises(ssd.SSDError, match="INVALID_ARG"):
         call(q=off)
