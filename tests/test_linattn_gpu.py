@@ -394,6 +394,32 @@ def test_a_page_named_twice_and_pages_out_of_range(ssd, cuda_dev):
     assert torch.equal(pool, one) and torch.equal(pool[[0, 1, 3]], before[[0, 1, 3]])
 
 
+@pytest.mark.parametrize("shift", [0, 1, 3])
+def test_large_batches_of_small_states(ssd, cuda_dev, shift):
+    """Several rows in one block; a page named again far down the list, which may start anywhere."""
+    b, H, K, V = 1030, 3, 16, 24
+    d = make(cuda_dev, [1] * b, torch.float32, H, H, K, V, seed=21)
+    ids = torch.randperm(b + 10, device=cuda_dev)[:b].int()
+    pool = torch.zeros(b + 10, H, V, K, device=cuda_dev)
+    pool[ids.long()] = d["s0"]
+    hold = torch.empty(b + shift, dtype=torch.int32, device=cuda_dev)
+    pages = hold[shift:]
+    pages.copy_(ids)
+    ref = LO.linattn(d["q"], d["k"], d["v"], d["ld"], K ** -0.5, d["s0"], [1] * b)
+    twice = [(1029, 0), (1000, 640)]                 # these rows name the pages of those
+    for late, early in twice:
+        pages[late] = pages[early]
+    before = pool.clone()
+    o = ssd.linear_attn_update(pool, d["q"], d["k"], d["v"], d["ld"], pages=pages, o=torch.full((b, H, V), 5.0, device=cuda_dev))
+    with pytest.raises(ssd.SSDError, match="INVALID_ARG"):
+        ssd.device_status()
+    ok = torch.ones(b, dtype=torch.bool, device=cuda_dev)
+    for late, _ in twice:
+        ok[late] = False
+        assert bool((o[late] == 5.0).all()) and torch.equal(pool[ids[late]], before[ids[late]])
+    check(o[ok], pool[ids.long()][ok], {n: t[ok] for n, t in ref.items()}, torch.float32, K, 1)
+
+
 def test_offsets_past_32_bits(ssd, cuda_dev):
     """A pool of 2^31 state elements and more: single tokens and prompts on its last pages."""
     H, K, V, n = 64, 128, 128, 2100                  # 4 MiB a page, 8.8 GB
