@@ -11,6 +11,7 @@
 #include <atomic>
 #include <mutex>
 #include <string>
+#include <type_traits>
 #include <vector>
 
 #include <cudaTypedefs.h>
@@ -56,14 +57,14 @@ ssd_status cuda_fail(cudaError_t e, const char* what) {
 enum Stage { ST_TABLE, ST_CUMSUM, ST_CHUNK_STATE, ST_STATE_PASSING, ST_CHUNK_SCAN, ST_STATE_UPDATE,
              ST_CONV, ST_CONV_UPDATE, ST_NORM, ST_STRICT_CUMSUM, ST_STRICT_STATE, ST_STRICT_PASSING,
              ST_STRICT_SCAN, ST_STRICT_CACHE, ST_STRICT_UPDATE, ST_STRICT_FOLD, ST_LA_STATE, ST_LA_PASSING, ST_LA_SCAN, ST_LA_UPDATE,
-             ST_PAGES_PLAN, ST_PAGES_MOVE, ST_COUNT };
+             ST_LA_STEPS,             ST_PAGES_PLAN, ST_PAGES_MOVE, ST_COUNT };
 const char* const kStageName[ST_COUNT] = {"ssd_chunk_table", "ssd_chunk_cumsum", "ssd_chunk_state",
                                           "ssd_state_passing", "ssd_chunk_scan", "ssd_state_update", "ssd_conv1d", "ssd_conv1d_update",
                                           "ssd_gated_rmsnorm", "ssd_strict_cumsum", "ssd_strict_chunk_state",
                                           "ssd_strict_state_passing", "ssd_strict_chunk_scan",
                                           "ssd_strict_cache_fill", "ssd_strict_state_update",
                                           "ssd_strict_fold", "ssd_linear_attn_state", "ssd_linear_attn_passing", "ssd_linear_attn_scan",
-                                          "ssd_linear_attn_update", "ssd_pages_plan", "ssd_pages_move"};
+                                          "ssd_linear_attn_update", "ssd_linear_attn_steps", "ssd_pages_plan", "ssd_pages_move"};
 constexpr size_t kMaxRecords = 65536;
 
 struct Profiler {
@@ -1367,6 +1368,9 @@ int la_segment_tokens(const LaPlan& p) {
     return (int)(ls * kC);
 }
 
+// Sequences of up to this many tokens go token by token.
+constexpr int kLaSteps = 64;
+
 ssd_status la_check(const ssd_linear_attn_dims* d, bool varlen, LaPlan* out) {
     if (!d) return fail(SSD_ERR_INVALID_ARG, "dims is NULL");
     if (d->nheads <= 0 || d->nkvheads <= 0 || d->headdim_k <= 0 || d->headdim_v <= 0)
@@ -1425,7 +1429,14 @@ ssd_status la_plan(const ssd_linear_attn_dims* d, bool varlen, LaPlan* out) {
     la::Args& a = p.a;
     a.Ls = la_segment_tokens(p);
     a.nps = varlen ? 0 : (int32_t)std::max<int64_t>(1, (a.seqlen + a.Ls - 1) / a.Ls);
-    p.max_segs = varlen ? p.T / a.Ls + a.nseq : (int64_t)a.nseq * a.nps;
+    // Short sequences go token by token: a dense batch of them, or those of a packed call whose
+    // mean length makes some likely (a call without any pays for one launch).
+    a.least = -1;
+    if (varlen ? p.T <= 8 * (int64_t)kLaSteps * a.nseq : a.seqlen <= kLaSteps) a.least = kLaSteps;
+    if (varlen) p.max_segs = p.T / a.Ls + (a.least >= 0 ? std::min<int64_t>(a.nseq, p.T / (a.least + 1)) : a.nseq);
+    else p.max_segs = a.least >= 0 ? 0 : (int64_t)a.nseq * a.nps;
+    if (a.least >= 0 && (int64_t)a.nseq * a.Hk * a.V >= INT32_MAX)
+        return fail(SSD_ERR_UNSUPPORTED, "too many sequences in one call");
     if (p.max_segs * a.Hk * ((a.V + 63) / 64) >= INT32_MAX) return fail(SSD_ERR_UNSUPPORTED, "too many segments in one call");
     size_t off = 0;
     auto take = [&](size_t bytes) {
@@ -1442,8 +1453,9 @@ ssd_status la_plan(const ssd_linear_attn_dims* d, bool varlen, LaPlan* out) {
     }
     // A state slot per segment and one per sequence. Without a second segment anywhere the
     // CUDA-core kernel uses none.
+    const int64_t slots = a.least >= 0 ? 2 * p.max_segs : p.max_segs + a.nseq;
     if (p.bf16 || (varlen ? p.T > a.Ls : a.nps > 1))
-        p.off_slots = take(sizeof(float) * (size_t)(p.max_segs + a.nseq) * a.Hk * a.V * a.K);
+        p.off_slots = take(sizeof(float) * (size_t)slots * a.Hk * a.V * a.K);
     p.bytes = std::max<size_t>(off, 256);
     return SSD_OK;
 }
@@ -1504,12 +1516,22 @@ void launch_la_update(const LaPlan& p, float* state, const int32_t* pages, int64
         a.R, a.K, a.V, a.q_stride, a.k_stride, a.v_stride);
 }
 
-template <typename T>
-void dispatch_la_update(const LaPlan& p, float* state, const int32_t* pages, int64_t batch, cudaStream_t st) {
-    if (p.a.K <= 16) launch_la_update<T, 4>(p, state, pages, batch, st);
-    else if (p.a.K <= 32) launch_la_update<T, 8>(p, state, pages, batch, st);
-    else if (p.a.K <= 64) launch_la_update<T, 16>(p, state, pages, batch, st);
-    else launch_la_update<T, 32>(p, state, pages, batch, st);
+template <typename T, int LPR>
+void launch_la_steps(const LaPlan& p, cudaStream_t st) {
+    const la::Args& a = p.a;
+    constexpr int rows = la::kTokRows * (32 / LPR), warps = la::kTokThreads / 32;
+    const int nvs = (a.V + rows - 1) / rows;
+    StageScope sc(ST_LA_STEPS, st);
+    la::k_la_steps<T, LPR><<<(unsigned)(((int64_t)a.nseq * a.Hk * nvs + warps - 1) / warps), la::kTokThreads, 0, st>>>(a, nvs);
+}
+
+// f with the lanes of a state row of K floats, 16 bytes a lane.
+template <typename F>
+void by_row_lanes(const LaPlan& p, F f) {
+    if (p.a.K <= 16) f(std::integral_constant<int, 4>{});
+    else if (p.a.K <= 32) f(std::integral_constant<int, 8>{});
+    else if (p.a.K <= 64) f(std::integral_constant<int, 16>{});
+    else f(std::integral_constant<int, 32>{});
 }
 
 }  // namespace
@@ -1551,7 +1573,7 @@ extern "C" ssd_status ssd_linear_attn_fwd(const void* q, const void* k, const vo
     }
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     // The tensor-core output pass needs the state pass for a final state too.
-    const bool many = cu_seqlens ? p.T > a.Ls : a.nps > 1, two_pass = many || (p.bf16 && final_state);
+    const bool many = p.max_segs > 0 && (cu_seqlens ? p.T > a.Ls : a.nps > 1), two_pass = many || (p.max_segs > 0 && p.bf16 && final_state);
     char* ws = static_cast<char*>(dims->workspace);
     bool owned = false;
     if (ws) {
@@ -1575,9 +1597,10 @@ extern "C" ssd_status ssd_linear_attn_fwd(const void* q, const void* k, const vo
     a.o = o;
     a.slots = reinterpret_cast<float*>(ws + p.off_slots);
     a.two_pass = two_pass;
+    a.cu = cu_seqlens;
     int n = 0;
     LaMaps maps;
-    if (p.bf16 && !la_maps(p, &maps)) s = fail(SSD_ERR_CUDA, "cuTensorMapEncodeTiled failed (q/k/v/o tensor maps)");
+    if (p.bf16 && p.max_segs > 0 && !la_maps(p, &maps)) s = fail(SSD_ERR_CUDA, "cuTensorMapEncodeTiled failed (q/k/v/o tensor maps)");
     if (s == SSD_OK && cu_seqlens) {
         auto* table = reinterpret_cast<ChunkEntry*>(ws + p.off_table);
         auto* first = reinterpret_cast<int32_t*>(ws + p.off_first);
@@ -1589,7 +1612,7 @@ extern "C" ssd_status ssd_linear_attn_fwd(const void* q, const void* k, const vo
         a.order = order;
         StageScope sc(ST_TABLE, st);
         k_chunk_table<<<1, kTableThreads, 0, st>>>(cu_seqlens, a.nseq, p.T, 0, a.Ls, table, first, count, 0, nullptr, order,
-                                                   nullptr, nullptr, true);
+                                                   nullptr, nullptr, a.least + 1);
         ++n;
     }
     if (s == SSD_OK && two_pass) {
@@ -1603,8 +1626,15 @@ extern "C" ssd_status ssd_linear_attn_fwd(const void* q, const void* k, const vo
         la::k_la_passing<<<grid, la::kPassThreads, 0, st>>>(a);
         ++n;
     }
-    if (s == SSD_OK) {
+    if (s == SSD_OK && p.max_segs > 0) {
         s = launch_la<true>(p, maps, p.max_segs, st);
+        ++n;
+    }
+    if (s == SSD_OK && a.least >= 0) {
+        by_row_lanes(p, [&](auto lpr) {
+            if (p.bf16) launch_la_steps<__nv_bfloat16, decltype(lpr)::value>(p, st);
+            else launch_la_steps<float, decltype(lpr)::value>(p, st);
+        });
         ++n;
     }
     cudaError_t e = cudaGetLastError();
@@ -1648,8 +1678,10 @@ extern "C" ssd_status ssd_linear_attn_update(float* state, const void* q, const 
     a.scale = scale;
     a.o = o;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (p.bf16) dispatch_la_update<__nv_bfloat16>(p, state, pages, a.nseq, st);
-    else dispatch_la_update<float>(p, state, pages, a.nseq, st);
+    by_row_lanes(p, [&](auto lpr) {
+        if (p.bf16) launch_la_update<__nv_bfloat16, decltype(lpr)::value>(p, state, pages, a.nseq, st);
+        else launch_la_update<float, decltype(lpr)::value>(p, state, pages, a.nseq, st);
+    });
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "kernel launch (linear attention update)");
     t_launches = 1;

@@ -41,11 +41,13 @@ struct Args {
     const int32_t* first;
     const int32_t* count;
     const int32_t* order;
+    const int32_t* cu;           // packed: cu_seqlens
     int64_t q_stride, k_stride, v_stride;   // elements between tokens
     int64_t seqlen, npages;
     float scale;
     int32_t nseq, nps;           // dense: segments per sequence
     int32_t Ls;                  // tokens per segment
+    int32_t least;               // packed: sequences of up to `least` tokens go token by token (-1: none do)
     int32_t H, Hk, R, K, V;
     bool two_pass;               // a state pass ran before the output pass
     bool stall;                  // test hook: a wait of the tensor-core kernel's UMMA warp runs out
@@ -61,6 +63,12 @@ struct Seg {
     int64_t start;
 };
 
+// First state slot of sequence s, whose segments begin with number `first`. Sequences that go
+// token by token have no segments and are many: the others then take two slots per segment.
+__device__ __forceinline__ int32_t slot_of(const Args& a, int32_t first, int32_t s) {
+    return a.table && a.least >= 0 ? 2 * first : first + s;
+}
+
 // Segment `i` of a pass; false where a packed call has fewer. `last`: the pass takes each
 // sequence's last segment too.
 __device__ __forceinline__ bool find_seg(const Args& a, int i, bool last, Seg* s) {
@@ -71,7 +79,7 @@ __device__ __forceinline__ bool find_seg(const Args& a, int i, bool last, Seg* s
         s->start = e.start;
         s->len = e.len;
         const int first = a.first[e.seq];
-        s->slot0 = first + e.seq;
+        s->slot0 = slot_of(a, first, e.seq);
         s->n = a.first[e.seq + 1] - first;
         s->j = e.pad - first;
         return last || s->j + 1 < s->n;
@@ -99,17 +107,18 @@ __device__ __noinline__ int64_t page_of(const int32_t* pages, int64_t npages, in
 }
 
 // Whether sequence s must not write its final state to page p: an earlier sequence writes
-// the same page, or another one starts from it in this call. Called by the whole block.
-__device__ __noinline__ bool page_clash(const Args& a, int32_t s, int64_t p, int threads) {
+// the same page, or another one starts from it in this call. Each of `step` threads looks
+// at its share; the caller joins what they find.
+__device__ __noinline__ int page_clash(const Args& a, int32_t s, int64_t p, int from, int step) {
     int bad = 0;
     const bool one_pool = a.init == a.fin;
-    if (!a.fin_pages && !(a.init_pages && one_pool)) return false;
-    for (int32_t i = threadIdx.x; i < a.nseq; i += threads) {
+    if (!a.fin_pages && !(a.init_pages && one_pool)) return 0;
+    for (int32_t i = from; i < a.nseq; i += step) {
         if (i == s) continue;
         if (i < s && a.fin_pages && a.fin_pages[i] == p) bad = 1;
         if (one_pool && (a.init_pages ? a.init_pages[i] : i) == p) bad = 1;
     }
-    return __syncthreads_or(bad) != 0;
+    return bad;
 }
 
 // lam^n in 64 bits. Not inlined: the prompt kernels take it at six places, and code that runs
@@ -140,13 +149,13 @@ __global__ void __launch_bounds__(kPassThreads) k_la_passing(const __grid_consta
     const int e = 4 * (blockIdx.z * kPassThreads + threadIdx.x), size = a.V * a.K;
     int first = s * a.nps, n = a.nps;
     if (a.table) {
-        if (*a.count == 0) return;                                // a bad cu_seqlens
+        if (*a.count <= 0) return;                                // a bad cu_seqlens, or no segments
         first = a.first[s];
         n = a.first[s + 1] - first;
     }
     if (e >= size || n < 2) return;
     const int64_t per_state = (int64_t)a.Hk * size;
-    float* p = a.slots + (int64_t)(first + s) * per_state + (int64_t)g * size + e;
+    float* p = a.slots + (int64_t)slot_of(a, first, s) * per_state + (int64_t)g * size + e;
     const float2 lam = pow2f(a.log_decay[g], a.Ls);
     const bool init = a.init && page_of(a.init_pages, a.npages, s) >= 0;
     float4 x = init ? *reinterpret_cast<const float4*>(p) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -270,7 +279,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) k_la_simt(const __grid_consta
     int64_t fp = -1;
     if (OUT && sg.j + 1 == sg.n && a.fin) {
         fp = page_of(a.fin_pages, a.npages, sg.seq);
-        if (fp >= 0 && page_clash(a, sg.seq, fp, NT)) {
+        if (fp >= 0 && __syncthreads_or(page_clash(a, sg.seq, fp, threadIdx.x, NT))) {
             latch_error(SSD_ERR_INVALID_ARG);
             fp = -1;
         }
@@ -415,6 +424,35 @@ __global__ void __launch_bounds__(kSimtThreads, 2) k_la_simt(const __grid_consta
 constexpr int kTokThreads = 128;    // warps are independent
 constexpr int kTokRows = 8;          // state rows in flight per lane group
 
+// Sums of kTokRows values per lane over the LPR lanes of a group. While more than one row is
+// left per lane, a lane gives half of its rows to its partner (8/2, 8/4, .. shuffles instead of
+// 8 per step); then plain butterflies. d[0 .. rows_left) are rows `returned` and on; with more
+// than eight lanes they are in every (LPR / 8)-th lane.
+__host__ __device__ constexpr int rows_left(int lpr) { return lpr >= kTokRows ? 1 : kTokRows / lpr; }
+
+template <int LPR>
+__device__ __forceinline__ int sum_rows(float (&d)[kTokRows], int c4) {
+    int n = kTokRows, off = LPR / 2, mine = 0;
+#pragma unroll
+    for (int step = 0; step < 3; ++step) {
+        if (off >= 1 && n > 1) {
+            const bool up = (c4 & off) != 0;
+#pragma unroll
+            for (int i = 0; i < kTokRows / 2; ++i)
+                if (i < n / 2) {
+                    const float give = up ? d[i] : d[i + n / 2], keep = up ? d[i + n / 2] : d[i];
+                    d[i] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+                }
+            n /= 2;
+            mine += up ? n : 0;
+            off /= 2;
+        }
+    }
+#pragma unroll
+    for (int w = LPR / 16; w >= 1; w /= 2) d[0] += __shfl_xor_sync(0xffffffffu, d[0], w);
+    return mine;
+}
+
 template <typename T, int LPR>
 __global__ void __launch_bounds__(kTokThreads)
 k_la_update(float* __restrict__ state, const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
@@ -485,37 +523,119 @@ k_la_update(float* __restrict__ state, const T* __restrict__ q, const T* __restr
         float d[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) d[u] = fmaf(s[u].x, qv.x, fmaf(s[u].y, qv.y, fmaf(s[u].z, qv.z, s[u].w * qv.w)));
-        // Sum over the LPR lanes of a group. While more than one row is left per lane, a
-        // lane gives half of its rows to its partner (U, U/2, .. shuffles in all instead
-        // of U per step); then plain butterflies.
-        int n = U, off = LPR / 2, mine = 0;
-#pragma unroll
-        for (int st2 = 0; st2 < 3; ++st2) {
-            if (off >= 1 && n > 1) {
-                const bool up = (c4 & off) != 0;
-#pragma unroll
-                for (int i = 0; i < U / 2; ++i)
-                    if (i < n / 2) {
-                        const float give = up ? d[i] : d[i + n / 2], keep = up ? d[i + n / 2] : d[i];
-                        d[i] = keep + __shfl_xor_sync(0xffffffffu, give, off);
-                    }
-                n /= 2;
-                mine += up ? n : 0;
-                off /= 2;
-            }
-        }
-#pragma unroll
-        for (int w = LPR / 16; w >= 1; w /= 2) d[0] += __shfl_xor_sync(0xffffffffu, d[0], w);
-        // each lane group's lanes with the low bits clear hold rows mine .. mine + n - 1
+        const int mine = sum_rows<LPR>(d, c4);
         if (LPR <= 8 || (c4 & (LPR / 8 - 1)) == 0) {
 #pragma unroll
-            for (int i = 0; i < U; ++i)
-                if (i < n) {
-                    const int row = r0 + (mine + i) * GPW;
-                    if (row < V) ob[(int64_t)r * V + row] = from_f32<T>(scale * d[i]);
-                }
+            for (int i = 0; i < rows_left(LPR); ++i) {
+                const int row = r0 + (mine + i) * GPW;
+                if (row < V) ob[(int64_t)r * V + row] = from_f32<T>(scale * d[i]);
+            }
         }
     }
+}
+
+// ---------------------------------------------------------------------------------
+// Short sequences of a prompt call, token by token: the same recurrence, the state in registers
+// from the sequence's first token to its last, so that it crosses HBM twice however many tokens
+// there are. A warp holds 8 to 64 rows of one state (a lane eight neighbouring rows, four columns) and
+// needs nothing from other warps; the next token's q, k and v are on their way while one is
+// computed. 4 K V FMAs a token where the chunked form has fewer and tensor cores for them, but
+// no CTA of it starts and ends in less than 25 us per 64 columns of V.
+template <typename T> struct Raw;                        // elements as they are loaded
+template <> struct Raw<float> {
+    float4 x{};
+    __device__ __forceinline__ void load(const float* p) { x = *reinterpret_cast<const float4*>(p); }
+    __device__ __forceinline__ float4 four() const { return x; }
+};
+template <> struct Raw<__nv_bfloat16> {
+    uint2 x{};
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { x = *reinterpret_cast<const uint2*>(p); }
+    __device__ __forceinline__ float4 four() const {
+        return make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u), __uint_as_float(x.y << 16),
+                           __uint_as_float(x.y & 0xffff0000u));
+    }
+};
+
+template <typename T, int LPR>
+__global__ void __launch_bounds__(kTokThreads) k_la_steps(const __grid_constant__ Args a, int nvs) {
+    constexpr int U = kTokRows, RPW = U * (32 / LPR);
+    const int lane = threadIdx.x & 31, c4 = lane % LPR, grp = lane / LPR;
+    const int64_t unit = (int64_t)blockIdx.x * (kTokThreads / 32) + (threadIdx.x >> 5);
+    const int Hk = a.Hk, K = a.K, V = a.V, R = a.R;
+    if (unit / nvs / Hk >= a.nseq) return;
+    const int32_t seq = (int32_t)(unit / nvs / Hk);
+    const int g = (int)(unit / nvs % Hk), row = (int)(unit % nvs) * RPW + grp * U;
+    int64_t start = seq * a.seqlen;
+    int32_t len = (int32_t)a.seqlen;
+    if (a.cu) {
+        if (*a.count < 0) return;                        // a bad cu_seqlens
+        start = a.cu[seq];
+        len = a.cu[seq + 1] - (int32_t)start;
+        if (len > a.least) return;
+    }
+    const bool col = 4 * c4 < K, rows = row < V, mine_ = col && rows;
+    const int64_t ip = a.init ? page_of(a.init_pages, a.npages, seq) : -1;
+    int64_t fp = a.fin ? page_of(a.fin_pages, a.npages, seq) : -1;
+    if (fp >= 0 && __any_sync(0xffffffffu, page_clash(a, seq, fp, lane, 32))) {
+        if (lane == 0) latch_error(SSD_ERR_INVALID_ARG);
+        fp = -1;
+    }
+    const int64_t at = ((int64_t)g * V + row) * K + 4 * c4, per_state = (int64_t)Hk * V * K;
+    float4 s[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        s[u] = mine_ && ip >= 0 ? __ldcs(reinterpret_cast<const float4*>(a.init + ip * per_state + at + u * K)) : make_float4(0, 0, 0, 0);
+    const T* qp = static_cast<const T*>(a.q) + start * a.q_stride + (int64_t)g * R * K + 4 * c4;
+    const T* kp = static_cast<const T*>(a.k) + start * a.k_stride + (int64_t)g * K + 4 * c4;
+    const T* vp = static_cast<const T*>(a.v) + start * a.v_stride + (int64_t)g * V + row;
+    T* op = static_cast<T*>(a.o) + (start * a.H + (int64_t)g * R) * V + row;
+    const float gd = a.log_decay[g];
+    if (lane == 0) check_decay(gd);
+    const float m1 = expm1f(gd), hi = 1.f + m1, lo = m1 - (hi - 1.f);        // lam = hi + lo
+    Raw<T> qn, kn, vn[2];
+    auto load_kv = [&] {
+        if (col) kn.load(kp);
+        if (rows) {
+            vn[0].load(vp);
+            vn[1].load(vp + 4);
+        }
+        kp += a.k_stride;
+        vp += a.v_stride;
+    };
+    if (len > 0) {
+        load_kv();
+        if (col) qn.load(qp);
+    }
+#pragma unroll 1
+    for (int t = 0; t < len; ++t, op += (int64_t)a.H * V) {
+        const float4 kv = kn.four(), va = vn[0].four(), vb = vn[1].four();
+        const float v[U] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
+        if (t + 1 < len) load_kv();
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            s[u].x = fmaf(hi, s[u].x, fmaf(lo, s[u].x, v[u] * kv.x));
+            s[u].y = fmaf(hi, s[u].y, fmaf(lo, s[u].y, v[u] * kv.y));
+            s[u].z = fmaf(hi, s[u].z, fmaf(lo, s[u].z, v[u] * kv.z));
+            s[u].w = fmaf(hi, s[u].w, fmaf(lo, s[u].w, v[u] * kv.w));
+        }
+#pragma unroll 1
+        for (int r = 0; r < R; ++r) {
+            const float4 qv = qn.four();
+            if (r + 1 == R) qp += a.q_stride;
+            if (col && (r + 1 < R || t + 1 < len)) qn.load(qp + (r + 1 < R ? (r + 1) * K : 0));
+            float d[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) d[u] = fmaf(s[u].x, qv.x, fmaf(s[u].y, qv.y, fmaf(s[u].z, qv.z, s[u].w * qv.w)));
+            const int mine = sum_rows<LPR>(d, c4);
+            if (rows && (LPR <= 8 || (c4 & (LPR / 8 - 1)) == 0)) {
+#pragma unroll
+                for (int i = 0; i < rows_left(LPR); ++i) op[(int64_t)r * V + mine + i] = from_f32<T>(a.scale * d[i]);
+            }
+        }
+    }
+    if (mine_ && fp >= 0)
+#pragma unroll
+        for (int u = 0; u < U; ++u) __stcs(reinterpret_cast<float4*>(a.fin + fp * per_state + at + u * K), s[u]);
 }
 
 }  // namespace la

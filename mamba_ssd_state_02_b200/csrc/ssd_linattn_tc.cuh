@@ -422,7 +422,7 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
     int64_t fp = -1;
     if (a.fin && sg.j + 1 == sg.n) {
         fp = page_of(a.fin_pages, a.npages, sg.seq);
-        if (fp >= 0 && page_clash(a, sg.seq, fp, kOutThreads)) {
+        if (fp >= 0 && __syncthreads_or(page_clash(a, sg.seq, fp, threadIdx.x, kOutThreads))) {
             latch_error(SSD_ERR_INVALID_ARG);
             fp = -1;
         }

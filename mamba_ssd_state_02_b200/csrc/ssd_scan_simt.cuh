@@ -28,8 +28,10 @@ namespace ssd {
 // With `order` (entries of at most 128 chunks of 128 tokens), order[k] is the entry the
 // k-th CTA of a pass takes: longest entries first (by 128-token chunks), so that CTAs of
 // unequal length finish together (longest-processing-time-first scheduling).
-// An entry's `pad` holds its index in the table. With `keep_empty` a sequence without tokens
-// has one entry of length 0 (its final state still has to be written); otherwise none. With `sub_first` (entries of the
+// An entry's `pad` holds its index in the table. A sequence of fewer than min_len tokens has no
+// entry; min_len 0: one without tokens has an entry of length 0 (its final state still has to be
+// written). With another min_len than 1 a bad cu_seqlens sets the count to -1, to tell it from a
+// call of short sequences only. With `sub_first` (entries of the
 // tensor-core pipeline and state snapshots every `snap` tokens, snap a multiple of 128),
 // every entry is further cut at the multiples of snap that fall inside it (positions
 // counted from its sequence's start) into sub-segments, numbered in token order over the
@@ -70,7 +72,7 @@ k_chunk_table(const int32_t* __restrict__ cu, int32_t nseq, int64_t T, int64_t s
               ChunkEntry* __restrict__ table, int32_t* __restrict__ first,
               int32_t* __restrict__ count, int64_t snap, int32_t* __restrict__ snap_first,
               int32_t* __restrict__ order = nullptr, int32_t* __restrict__ sub_first = nullptr,
-              int32_t* __restrict__ sub_end = nullptr, bool keep_empty = false) {
+              int32_t* __restrict__ sub_end = nullptr, int64_t min_len = 1) {
     static_assert(kTableThreads == 32 * 32, "table_scan assumes 32 warps");
     __shared__ int32_t wsum[3][32];
     const int tid = threadIdx.x;
@@ -87,11 +89,12 @@ k_chunk_table(const int32_t* __restrict__ cu, int32_t nseq, int64_t T, int64_t s
     if (bad) {
         if (tid == 0) latch_error(SSD_ERR_INVALID_ARG);
         for (int s = tid; s <= nseq; s += kTableThreads) first[s] = 0;
-        if (tid == 0) *count = 0;
+        if (tid == 0) *count = min_len == 1 ? 0 : -1;
         return;
     }
     int32_t local = 0;
-    auto entries = [&](int64_t len) -> int32_t { return keep_empty && len == 0 ? 1 : (int32_t)((len + Q - 1) / Q); };
+    // Sequences of fewer than min_len tokens have no entry, other empty ones have one.
+    auto entries = [&](int64_t len) -> int32_t { return len < min_len ? 0 : len == 0 ? 1 : (int32_t)((len + Q - 1) / Q); };
     for (int s = s0; s < s1; ++s) local += entries(seq_begin(s + 1) - seq_begin(s));
     int32_t nent = 0;
     int32_t run = table_scan(local, wsum[0], &nent);

@@ -85,6 +85,19 @@ def test_packed_prompts(ssd, cuda_dev, H, Hk, K, V, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("H,Hk,K,V", HEADS)
+@pytest.mark.parametrize("lens", [[1] * 9, [64, 65, 0, 63, 7, 400], [2500, 1, 0, 33, 64, 130], [64] * 3 + [900]])
+def test_short_sequences_among_long_ones(ssd, cuda_dev, H, Hk, K, V, dtype, lens):
+    """Short sequences go token by token or, where they are few, through the chunks."""
+    d = make(cuda_dev, lens, dtype, H, Hk, K, V, seed=17)
+    ref = LO.linattn(d["q"], d["k"], d["v"], d["ld"], K ** -0.5, d["s0"], lens)
+    state = d["s0"].clone()
+    o, fin = ssd.linear_attn_fwd(d["q"], d["k"], d["v"], d["ld"], init_state=state, final_state=state, cu_seqlens=cu_of(lens, cuda_dev))
+    ssd.device_status()
+    check(o, fin, ref, dtype, K, max(lens))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("b,L", [(1, 1), (3, 63), (2, 128), (1, 385), (2, 700)])
 def test_dense_prompts(ssd, cuda_dev, b, L, dtype):
     H, Hk, K, V = 6, 3, 64, 128
