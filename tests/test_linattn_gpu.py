@@ -86,7 +86,7 @@ def test_packed_prompts(ssd, cuda_dev, H, Hk, K, V, dtype):
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("H,Hk,K,V", HEADS)
-@pytest.mark.parametrize("lens", [[1] * 9, [64, 65, 0, 63, 7, 400], [2500, 1, 0, 33, 64, 130], [64] * 3 + [900]])
+@pytest.mark.parametrize("lens", [[1] * 9, [64, 65, 0, 63, 7, 400], [32, 33, 0, 31, 7, 300], [2500, 1, 0, 33, 64, 130], [32] * 8 + [900]])
 def test_short_sequences_among_long_ones(ssd, cuda_dev, H, Hk, K, V, dtype, lens):
     """Short sequences go token by token or, where they are few, through the chunks."""
     d = make(cuda_dev, lens, dtype, H, Hk, K, V, seed=17)
