@@ -1510,12 +1510,12 @@ ssd_status launch_la(const LaPlan& p, const LaMaps& m, int64_t segs, cudaStream_
 template <typename T, int LPR>
 void launch_la_update(const LaPlan& p, float* state, const int32_t* pages, int64_t batch, cudaStream_t st) {
     const la::Args& a = p.a;
-    constexpr int rows = la::kTokRows * (32 / LPR), warps = la::kTokThreads / 32;
+    constexpr int rows = la::kTokRows * (32 / LPR) * (la::kTokThreads / 32);
     const int nvs = (a.V + rows - 1) / rows;
     StageScope sc(ST_LA_UPDATE, st);
-    la::k_la_update<T, LPR><<<(unsigned)((batch * a.Hk * nvs + warps - 1) / warps), la::kTokThreads, 0, st>>>(
-        state, (const T*)a.q, (const T*)a.k, (const T*)a.v, a.log_decay, a.scale, pages, a.npages, (T*)a.o, batch, nvs, a.Hk,
-        a.R, a.K, a.V, a.q_stride, a.k_stride, a.v_stride);
+    la::k_la_update<T, LPR><<<(unsigned)(batch * a.Hk * nvs), la::kTokThreads, 0, st>>>(
+        state, (const T*)a.q, (const T*)a.k, (const T*)a.v, a.log_decay, a.scale, pages, a.npages, (T*)a.o, nvs, a.Hk, a.R,
+        a.K, a.V, a.q_stride, a.k_stride, a.v_stride);
 }
 
 template <typename T, int LPR>

@@ -416,12 +416,11 @@ __global__ void __launch_bounds__(kSimtThreads, 2) k_la_simt(const __grid_consta
 // is all the traffic that counts, so the kernel is an HBM stream: a state row of K floats
 // is LPR lanes of 16 bytes, a warp keeps 8 rows per lane group in flight before it writes
 // any, and one state serves all R query heads that share it. 256 sequences of 32 heads (1.08 GB
-// of traffic): 166 us, 99% of the measured copy rate. A warp by itself is the unit (8 to 64 rows
-// of one state), so that blocks of small states have no idle warps: 16384 rows of two 4 KiB
-// states take 43 us (a block for each state: 75), 65536 rows of one 1 KiB state 51 us (143).
-// Finding pages named twice is quadratic in the batch: nothing to see at 256 rows, 11 us of 93
-// at 4096, most of the time at 65536 (a table of claims would need scratch and two launches).
-constexpr int kTokThreads = 128;    // warps are independent
+// of traffic): 165 us, 99% of the measured copy rate. A warp as the unit, each with its own
+// search for pages named twice, was 1.7 times as fast on 16384 rows of 4 KiB states, but took
+// 100 registers instead of 70 and 180 us of the case above. That search is quadratic in the batch:
+// nothing to see at 256 rows, 4 us of 86 at 4096, half of the time at 16384.
+constexpr int kTokThreads = 128;
 constexpr int kTokRows = 8;          // state rows in flight per lane group
 
 // Sums of kTokRows values per lane over the LPR lanes of a group. While more than one row is
@@ -457,25 +456,24 @@ template <typename T, int LPR>
 __global__ void __launch_bounds__(kTokThreads)
 k_la_update(float* __restrict__ state, const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
             const float* __restrict__ log_decay, float scale, const int32_t* __restrict__ pages, int64_t npages,
-            T* __restrict__ o, int64_t batch, int nvs, int Hk, int R, int K, int V, int64_t qs, int64_t ks, int64_t vs) {
+            T* __restrict__ o, int nvs, int Hk, int R, int K, int V, int64_t qs, int64_t ks, int64_t vs) {
     constexpr int GPW = 32 / LPR;                        // lane groups (rows of one load) per warp
-    constexpr int U = kTokRows, RPW = U * GPW;           // state rows per warp
-    const int lane = threadIdx.x & 31, c4 = lane % LPR, grp = lane / LPR;
-    const int64_t unit = (int64_t)blockIdx.x * (kTokThreads / 32) + (threadIdx.x >> 5);
-    const int64_t b = unit / nvs / Hk;
-    if (b >= batch) return;
-    const int vsp = (int)(unit % nvs), g = (int)(unit / nvs % Hk);
-    int32_t page = (int32_t)b;
+    constexpr int U = kTokRows, WARPS = kTokThreads / 32;
+    constexpr int RPB = U * GPW * WARPS;                 // state rows per CTA
+    const int vsp = blockIdx.x % nvs, g = (blockIdx.x / nvs) % Hk;
+    const int64_t b = blockIdx.x / nvs / Hk;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c4 = lane % LPR, grp = lane / LPR;
+    int64_t page = b;
     if (pages) {
         page = pages[b];
         if (page < 0 || page >= npages) {                // -1: a padded row, left as it is
-            if (page != -1 && lane == 0) latch_error(SSD_ERR_INVALID_ARG);
+            if (page != -1 && threadIdx.x == 0) latch_error(SSD_ERR_INVALID_ARG);
             return;
         }
     }
-    float* st = state + ((int64_t)page * Hk + g) * V * K;
+    float* st = state + (page * Hk + g) * (int64_t)V * K;
     // this lane group's rows: r0 + u * GPW, columns 4 c4 ..
-    const int r0 = vsp * RPW + grp;
+    const int r0 = vsp * RPB + warp * U * GPW + grp;
     const bool col = 4 * c4 < K;
     float4 s[U];
     float vr[U];
@@ -488,23 +486,17 @@ k_la_update(float* __restrict__ state, const T* __restrict__ q, const T* __restr
     }
     const float4 kv = col ? load4(k + b * ks + (int64_t)g * K + 4 * c4) : make_float4(0, 0, 0, 0);
     if (pages) {
-        // A page named twice would be updated by two warps at once: the first row keeps it, the
-        // others are refused.
+        // A page named twice would be updated by two blocks at once: the first row keeps
+        // it, the others are refused.
         int dup = 0;
-        const int64_t n4 = (reinterpret_cast<uintptr_t>(pages) & 15) == 0 ? b / 4 : 0;
-#pragma unroll 4
-        for (int64_t i = lane; i < n4; i += 32) {
-            const int4 p = reinterpret_cast<const int4*>(pages)[i];
-            dup |= p.x == page || p.y == page || p.z == page || p.w == page;
-        }
-        for (int64_t i = 4 * n4 + lane; i < b; i += 32) dup |= pages[i] == page;
-        if (__any_sync(0xffffffffu, dup)) {
-            if (lane == 0) latch_error(SSD_ERR_INVALID_ARG);
+        for (int64_t i = threadIdx.x; i < b; i += kTokThreads) dup |= pages[i] == page;
+        if (__syncthreads_or(dup)) {
+            if (threadIdx.x == 0) latch_error(SSD_ERR_INVALID_ARG);
             return;
         }
     }
     const float gd = log_decay[g];
-    if (lane == 0) check_decay(gd);
+    if (threadIdx.x == 0) check_decay(gd);
     // lam = hi + lo: 1 + expm1(g) with the rounding of the sum kept
     const float m1 = expm1f(gd), hi = 1.f + m1, lo = m1 - (hi - 1.f);
 #pragma unroll
@@ -523,13 +515,35 @@ k_la_update(float* __restrict__ state, const T* __restrict__ q, const T* __restr
         float d[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) d[u] = fmaf(s[u].x, qv.x, fmaf(s[u].y, qv.y, fmaf(s[u].z, qv.z, s[u].w * qv.w)));
-        const int mine = sum_rows<LPR>(d, c4);
+        // Sum over the LPR lanes of a group. While more than one row is left per lane, a
+        // lane gives half of its rows to its partner (U, U/2, .. shuffles in all instead
+        // of U per step); then plain butterflies.
+        int n = U, off = LPR / 2, mine = 0;
+#pragma unroll
+        for (int st2 = 0; st2 < 3; ++st2) {
+            if (off >= 1 && n > 1) {
+                const bool up = (c4 & off) != 0;
+#pragma unroll
+                for (int i = 0; i < U / 2; ++i)
+                    if (i < n / 2) {
+                        const float give = up ? d[i] : d[i + n / 2], keep = up ? d[i + n / 2] : d[i];
+                        d[i] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+                    }
+                n /= 2;
+                mine += up ? n : 0;
+                off /= 2;
+            }
+        }
+#pragma unroll
+        for (int w = LPR / 16; w >= 1; w /= 2) d[0] += __shfl_xor_sync(0xffffffffu, d[0], w);
+        // each lane group's lanes with the low bits clear hold rows mine .. mine + n - 1
         if (LPR <= 8 || (c4 & (LPR / 8 - 1)) == 0) {
 #pragma unroll
-            for (int i = 0; i < rows_left(LPR); ++i) {
-                const int row = r0 + (mine + i) * GPW;
-                if (row < V) ob[(int64_t)r * V + row] = from_f32<T>(scale * d[i]);
-            }
+            for (int i = 0; i < U; ++i)
+                if (i < n) {
+                    const int row = r0 + (mine + i) * GPW;
+                    if (row < V) ob[(int64_t)r * V + row] = from_f32<T>(scale * d[i]);
+                }
         }
     }
 }
@@ -563,11 +577,10 @@ template <typename T, int LPR>
 __global__ void __launch_bounds__(kTokThreads) k_la_steps(const __grid_constant__ Args a, int nvs) {
     constexpr int U = kTokRows, RPW = U * (32 / LPR);
     const int lane = threadIdx.x & 31, c4 = lane % LPR, grp = lane / LPR;
-    const int64_t unit = (int64_t)blockIdx.x * (kTokThreads / 32) + (threadIdx.x >> 5);
     const int Hk = a.Hk, K = a.K, V = a.V, R = a.R;
-    if (unit / nvs / Hk >= a.nseq) return;
-    const int32_t seq = (int32_t)(unit / nvs / Hk);
-    const int g = (int)(unit / nvs % Hk), row = (int)(unit % nvs) * RPW + grp * U;
+    const uint32_t unit = blockIdx.x * (kTokThreads / 32) + (threadIdx.x >> 5), part = unit / (uint32_t)nvs;   // < 2^31
+    const int seq = (int)(part / (uint32_t)Hk), g = (int)part - seq * Hk, row = (int)(unit - part * nvs) * RPW + grp * U;
+    if (seq >= a.nseq) return;
     int64_t start = seq * a.seqlen;
     int32_t len = (int32_t)a.seqlen;
     if (a.cu) {
