@@ -141,7 +141,7 @@ __device__ __forceinline__ void check_decay(float g) {
 // the copy of the initial state. One thread per four state elements, the loads of four
 // segments in flight ahead of the chain. (Each output CTA summing the segments before it
 // itself costs a pass over all their states per segment: with 64 segments the output pass took
-// ten times as long.)
+// ten times as long.) 4 to 12 us: latency.
 constexpr int kPassThreads = 256;
 
 __global__ void __launch_bounds__(kPassThreads) k_la_passing(const __grid_constant__ Args a) {
@@ -181,7 +181,9 @@ __global__ void __launch_bounds__(kPassThreads) k_la_passing(const __grid_consta
 // the inputs). One CTA per (segment, key/value head, 64 columns of V); chunks of 64 tokens in
 // shared memory, the state there too as [K][64]. Without OUT: only the state that the segment
 // adds. Every product runs in 4 x 4 register tiles fed by 16-byte shared loads along the
-// summed index, eight for 64 FMAs.
+// summed index, eight for 64 FMAs. Bound by those shared loads and by the wait for a chunk's rows
+// (two CTAs per SM hide each other's where their shared memory fits): 3 sequences of 1537 tokens
+// take 43 us (state) and 104 us (output), a lone CTA 5.5 us per chunk at K = V = 16, 10 at 64.
 constexpr int kSimtC = 64;           // tokens per chunk
 constexpr int kSimtV = 64;           // V columns per CTA
 constexpr int kSimtThreads = 256;
@@ -555,7 +557,7 @@ k_la_update(float* __restrict__ state, const T* __restrict__ q, const T* __restr
 // needs nothing from other warps; the next token's q, k and v are on their way while one is
 // computed. 4 K V FMAs a token where the chunked form has fewer and tensor cores for them, but
 // no CTA of it starts and ends in less than 25 us per 64 columns of V. 256 sequences of one token
-// (32 heads, 128 x 128): 178 us, 93% of the measured copy rate (in chunks 3540 us); of 16 tokens 852 us.
+// (32 heads, 128 x 128): 167 us, 99% of the measured copy rate (in chunks 3530 us); of 16 tokens 805 us.
 // Bound by instruction issue from a few tokens on (274 instructions a token and warp, 69% of the
 // issue slots). Packed pairs of FMAs and batches of four tokens were no faster.
 template <typename T> struct Raw;                        // elements as they are loaded

@@ -108,7 +108,9 @@ __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_
 // the state. K and V are triple-buffered; w V goes through two buffers of 64 tokens, so
 // that one is written while the UMMAs read the other; D is double-buffered. The three terms of
 // w V lie side by side as one N = 192 operand, so K is read once for them (97 cycles a step;
-// three N = 64 steps take 147, bound by the reads of their operands).
+// three N = 64 steps take 147, bound by the reads of their operands). 4 x 4096 tokens, 32 heads of
+// 128 x 128: 95 us (268 MB of k and v: 2.8 TB/s); tensor pipe 31%, DRAM 35%: bound by the chain
+// V -> w V -> D -> state.
 constexpr int kWriteWarps = 8;
 constexpr int kHalf = 64;                    // tokens of a w V buffer
 constexpr int kStateThreads = 32 * (4 + kWriteWarps + kStateWarps);
@@ -346,7 +348,8 @@ k_la_tc_state(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
 // Ox, warp 2 those of D (an issuing warp takes its batches in order, and the waits of one
 // product would hold up the others); then three groups of eight warps: scores and w V, outputs,
 // and the state. Q, K and V are double-buffered. Q K^T runs one unit ahead, in the gap that the
-// outputs leave in the tensor pipe while they are read.
+// outputs leave in the tensor pipe while they are read. 4 x 4096 tokens, 32 heads of 128 x 128:
+// 177 us (537 MB: 3.0 TB/s); tensor pipe 32%, DRAM 33%: bound by the chain scores -> P -> P V.
 //
 // Shared memory: K, V, Q (two buffers each), S (a bf16 pair), w V, and a tile of o on its way
 // out by TMA (a thread's row of o is 64 bytes in another line than its neighbours'; stored from
