@@ -698,11 +698,16 @@ def _token_stride(t, name, lead, heads, dim, dtype, device):
     if st[-1] != 1 or (heads > 1 and st[-2] != dim):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
     if len(lead) == 1:
-        return st[0] if lead[0] > 1 else heads * dim
-    b, L = lead
-    if b > 1 and L > 1 and st[0] != L * st[1]:
-        raise ValueError(f"{name}: the sequences of a dense batch must follow each other without a gap")
-    return st[1] if L > 1 else st[0] if b > 1 else heads * dim
+        step = st[0] if lead[0] > 1 else heads * dim
+    else:
+        b, L = lead
+        if b > 1 and L > 1 and st[0] != L * st[1]:
+            raise ValueError(f"{name}: the sequences of a dense batch must follow each other without a gap")
+        step = st[1] if L > 1 else st[0] if b > 1 else heads * dim
+    if step < heads * dim:
+        # An expanded tensor's 0 would mean "contiguous" to the library, which would read past its end.
+        raise ValueError(f"{name}: tokens that share memory (an expanded tensor?) must be made contiguous first")
+    return step
 
 
 def _pages_arg(pages, name, n, device):

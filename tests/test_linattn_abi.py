@@ -150,3 +150,38 @@ def test_binding_checks_before_the_library(ssd):
         ssd.linear_attn_update(torch.zeros(2, 4, 16, 16), z, z, z, torch.zeros(4))
     with pytest.raises(ValueError, match="array 0"):
         ssd.PagePool([z], 2, 2)
+
+
+class _OnDevice:
+    """The layout of a CPU tensor, as the binding's checks would see it on a device."""
+    is_cuda = True
+
+    def __init__(self, t):
+        self.t, self.shape, self.dtype, self.device = t, t.shape, t.dtype, t.device
+
+    def stride(self):
+        return self.t.stride()
+
+    def is_contiguous(self):
+        return self.t.is_contiguous()
+
+
+def test_token_strides(ssd):
+    """Expanded (stride 0) and overlapping tokens are refused: the library reads a stride of 0
+    as "contiguous"."""
+    import torch
+    H, K = 4, 16
+    step = lambda t: ssd._token_stride(_OnDevice(t), "q", t.shape[:-2], H, K, t.dtype, t.device)  # noqa: E731
+    one = torch.zeros(1, H, K)
+    for t in (one.expand(7, H, K), one.expand(2, 7, H, K), one.expand(1, 7, H, K), one[None].expand(5, 1, H, K),
+              torch.zeros(7 * H * K).as_strided((3, H, K), (H * K - 8, K, 1)),
+              torch.zeros(7 * H * K).as_strided((2, 3, H, K), (3 * K, K, K, 1))):
+        with pytest.raises(ValueError, match="share memory"):
+            step(t)
+    with pytest.raises(ValueError, match="without a gap"):
+        step(torch.zeros(1, 7, H, K).expand(2, 7, H, K))
+    row = torch.zeros(14, H * K + 8)[:, :H * K].unflatten(1, (H, K))
+    assert step(row) == H * K + 8 and step(row.unflatten(0, (2, 7))) == H * K + 8
+    assert step(row.unflatten(0, (14, 1))) == H * K + 8
+    for t in (one.expand(1, 1, H, K), one, torch.zeros(0, H, K), torch.zeros(2, 0, H, K), torch.zeros(3, 7, H, K)):
+        assert step(t) == H * K

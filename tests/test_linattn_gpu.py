@@ -617,3 +617,24 @@ def test_wait_runs_out_and_context_stays_usable(ssd, cuda_dev, stalled_pass):
     ssd.device_status()
     ref = LO.linattn(d["q"], d["k"], d["v"], d["ld"], K ** -0.5, d["s0"], lens)
     check(o, fin, ref, torch.bfloat16, K, 300)
+
+
+def test_expanded_inputs_are_refused(ssd, cuda_dev):
+    """Tokens that share memory: refused by the binding before any launch."""
+    H, Hk, K, V = 4, 2, 64, 64
+    d = make(cuda_dev, [12], torch.bfloat16, H, Hk, K, V)
+    one = {n: d[n][:1] for n in "qkv"}
+    cu = cu_of([12], cuda_dev)
+    state = torch.zeros(12, Hk, V, K, device=cuda_dev)
+    for n in "qkv":
+        wide = one[n].expand(12, *one[n].shape[1:])
+        packed = {**{m: d[m] for m in "qkv"}, n: wide}
+        with pytest.raises(ValueError, match="share memory"):
+            ssd.linear_attn_fwd(**packed, log_decay=d["ld"], cu_seqlens=cu)
+        for b, L in ((1, 12), (3, 4), (12, 1)):
+            with pytest.raises(ValueError, match="share memory"):
+                ssd.linear_attn_fwd(**{m: t.unflatten(0, (b, L)) if m != n else one[n].expand(b, L, *t.shape[1:])
+                                       for m, t in packed.items()}, log_decay=d["ld"])
+        with pytest.raises(ValueError, match="share memory"):
+            ssd.linear_attn_update(state, **packed, log_decay=d["ld"])
+    ssd.device_status()
