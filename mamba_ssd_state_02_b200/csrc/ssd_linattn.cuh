@@ -132,6 +132,15 @@ __device__ __forceinline__ float2 pow2f(float g, int64_t n) {
     return make_float2(hi, (float)(e - (double)hi));
 }
 
+// lam as hi + lo for a state that meets it once a token. Slow decays: 1 + expm1(g) with the
+// rounding of the sum kept, an error of 2^-24 of 1 - lam, so that it stays 2^-24 over the 1 / (1 - lam)
+// tokens that the state remembers. Below 1/2 that would be relative to 1 and not to lam (no digit is
+// left at g = -17), and the state remembers less than two tokens: exp(g) rounded to float.
+__device__ __forceinline__ float2 decay_pair(float g) {
+    const float m1 = expm1f(g), hi = 1.f + m1;
+    return m1 < -0.5f ? make_float2(expf(g), 0.f) : make_float2(hi, m1 - (hi - 1.f));
+}
+
 __device__ __forceinline__ void check_decay(float g) {
     if (!(g <= 0.f) || isinf(g)) latch_error(SSD_ERR_INVALID_ARG);
 }
@@ -499,8 +508,8 @@ k_la_update(float* __restrict__ state, const T* __restrict__ q, const T* __restr
     }
     const float gd = log_decay[g];
     if (threadIdx.x == 0) check_decay(gd);
-    // lam = hi + lo: 1 + expm1(g) with the rounding of the sum kept
-    const float m1 = expm1f(gd), hi = 1.f + m1, lo = m1 - (hi - 1.f);
+    const float2 lam = decay_pair(gd);
+    const float hi = lam.x, lo = lam.y;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int row = r0 + u * GPW;
@@ -557,7 +566,7 @@ k_la_update(float* __restrict__ state, const T* __restrict__ q, const T* __restr
 // needs nothing from other warps; the next token's q, k and v are on their way while one is
 // computed. 4 K V FMAs a token where the chunked form has fewer and tensor cores for them, but
 // no CTA of it starts and ends in less than 25 us per 64 columns of V. 256 sequences of one token
-// (32 heads, 128 x 128): 167 us, 99% of the measured copy rate (in chunks 3530 us); of 16 tokens 805 us.
+// (32 heads, 128 x 128): 167 us, 99% of the measured copy rate (in chunks 3530 us); of 16 tokens 824 us.
 // Bound by instruction issue from a few tokens on (274 instructions a token and warp, 69% of the
 // issue slots). Packed pairs of FMAs and batches of four tokens were no faster.
 template <typename T> struct Raw;                        // elements as they are loaded
@@ -609,7 +618,8 @@ __global__ void __launch_bounds__(kTokThreads) k_la_steps(const __grid_constant_
     T* op = static_cast<T*>(a.o) + (start * a.H + (int64_t)g * R) * V + row;
     const float gd = a.log_decay[g];
     if (lane == 0) check_decay(gd);
-    const float m1 = expm1f(gd), hi = 1.f + m1, lo = m1 - (hi - 1.f);        // lam = hi + lo
+    const float2 lam = decay_pair(gd);
+    const float hi = lam.x, lo = lam.y;
     Raw<T> qn, kn, vn[2];
     auto load_kv = [&] {
         if (col) kn.load(kp);

@@ -638,3 +638,35 @@ def test_expanded_inputs_are_refused(ssd, cuda_dev):
         with pytest.raises(ValueError, match="share memory"):
             ssd.linear_attn_update(state, **packed, log_decay=d["ld"])
     ssd.device_status()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("R", [1, 2])
+def test_the_decay_itself(ssd, cuda_dev, dtype, R):
+    """Keys of zero, so that a state is only decayed: final = lam^n S_0, for decays from none to
+    past the smallest float, one token at a time, in short prompts and in chunks.
+    Tolerance per token: exp and expm1 within one unit of their last place (2^-23 of lam; expm1 at
+    lam >= 1/2 half of that), the rest of the step three roundings of 2^-24, of which two only
+    touch the low part: below 2^-22. Where lam S_0 is subnormal: 2^-149 for a unit of lam and half
+    of it for each rounding, 2^-148 (1 + |S_0|) in all."""
+    decays = [0.0, -1e-6, -0.01, -0.5, -0.693, -0.6932, -0.7, -1.0, -3.0, -8.0, -12.0, -17.0, -20.0, -40.0, -80.0, -86.0, -95.0, -110.0]
+    Hk, K, V = len(decays), 24, 40
+    ld = torch.tensor(decays, device=cuda_dev)
+    g = torch.Generator().manual_seed(3)
+    r = lambda *s: torch.randn(*s, generator=g).to(dtype).to(cuda_dev)  # noqa: E731
+    for lens in ([1], [3, 1], [1, 600, 2]):                # the last through the chunks
+        T = sum(lens)
+        q, k, v = r(T, Hk * R, K), torch.zeros(T, Hk, K, dtype=dtype, device=cuda_dev), r(T, Hk, V)
+        s0 = r(len(lens), Hk, V, K).float()
+        _, fin = ssd.linear_attn_fwd(q, k, v, ld, init_state=s0, cu_seqlens=cu_of(lens, cuda_dev))
+        got = [(fin, lens)]
+        if lens == [1]:
+            state = s0.clone()
+            ssd.linear_attn_update(state, q, k, v, ld)
+            got.append((state, lens))
+        ssd.device_status()
+        for x, ns in got:
+            n = torch.tensor(ns, device=cuda_dev, dtype=torch.float64).view(-1, 1, 1, 1)
+            ref = s0.double() * torch.exp(n * ld.double().view(1, -1, 1, 1))
+            bad = (x.double() - ref).abs() > n * (2.0 ** -22 * ref.abs() + 2.0 ** -148 * (1 + s0.double().abs()))
+            assert not bool(bad.any()), (lens, [decays[i] for i in bad.any(3).any(2).any(0).nonzero().flatten().tolist()])
