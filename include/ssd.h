@@ -368,7 +368,11 @@ ssd_status ssd_linear_attn_fwd_workspace_size(const ssd_linear_attn_dims* dims, 
  *   scale: usually 1 / sqrt(K).
  * A NaN or infinity in k or v reaches every output of its sequence and key/value head from
  * the start of its 128-token chunk on (the chunk's products are dense); one in q reaches its
- * own token's outputs only. Other sequences never see it.
+ * own token's outputs only. Other sequences never see it. One in a state (given, or reached by
+ * overflow; single tokens too) stays in its own element of the state and reaches its head's
+ * outputs in its row of V. It may come out as NaN where the recurrence has an infinity: lam is
+ * kept as a sum of two floats, and 0 times infinity is not a number. An empty sequence's state
+ * is copied bit for bit.
  */
 ssd_status ssd_linear_attn_fwd(const void* q, const void* k, const void* v, const float* log_decay, float scale,
                                const float* init_state, const int32_t* init_pages, const int32_t* cu_seqlens,

@@ -767,8 +767,9 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
                     const int v = v_of(i), kk = k_of(i);
                     const uint32_t to = sS + kk * 256 + ((((uint32_t)v >> 2) ^ (kk & 15)) << 4) + (v & 3) * 4;
                     asm volatile("st.shared.f32 [%0], %1;" ::"r"(to), "f"(x[i]) : "memory");
+                    // an empty sequence's state as it is: 0 times an infinity would be NaN
                     if (fp >= 0 && mine(i))
-                        fin[v * K + kk] = fmaf(lam_len.x, x[i], fmaf(lam_len.y, x[i], slots[per_state + v * K + kk]));
+                        fin[v * K + kk] = nt == 0 ? x[i] : fmaf(lam_len.x, x[i], fmaf(lam_len.y, x[i], slots[per_state + v * K + kk]));
                 }
             }
             named_barrier(1, 32 * kStateWarps);

@@ -670,3 +670,50 @@ def test_the_decay_itself(ssd, cuda_dev, dtype, R):
             ref = s0.double() * torch.exp(n * ld.double().view(1, -1, 1, 1))
             bad = (x.double() - ref).abs() > n * (2.0 ** -22 * ref.abs() + 2.0 ** -148 * (1 + s0.double().abs()))
             assert not bool(bad.any()), (lens, [decays[i] for i in bad.any(3).any(2).any(0).nonzero().flatten().tolist()])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n", [20, 900])                   # token by token, and in chunks
+def test_states_of_empty_sequences_are_copied(ssd, cuda_dev, dtype, n):
+    lens, Hk, K, V = [0, n, 0, 0], 2, 64, 72
+    d = make(cuda_dev, lens, dtype, Hk, Hk, K, V, seed=4)
+    for i, x in enumerate((float("inf"), -float("inf"), float("nan"), -0.0, 1e-45, 3.4e38)):
+        d["s0"][0, :, 7 * i, 5 * i] = x
+        d["s0"][3, :, V - 1 - i, K - 1] = x
+    pages = torch.tensor([3, 1, -1, 0], dtype=torch.int32, device=cuda_dev)
+    for init, ip, want in ((d["s0"], None, d["s0"]), (d["s0"], pages, d["s0"][[3, 1, 2, 0]])):
+        _, fin = ssd.linear_attn_fwd(d["q"], d["k"], d["v"], d["ld"], init_state=init, init_pages=ip, cu_seqlens=cu_of(lens, cuda_dev))
+        ssd.device_status()
+        for s in (0, 3):
+            assert torch.equal(fin[s].view(torch.int32), want[s].view(torch.int32))
+        assert ip is None or not bool(fin[2].any())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_a_non_finite_state_stays_in_its_row(ssd, cuda_dev, dtype, bad):
+    """It makes its own element of the final state and its row of V in its head's outputs
+    non-finite; everything else is bit for bit what it is without it."""
+    H, Hk, K, V, hk, row, col = 4, 2, 64, 72, 1, 65, 9
+    hit = slice(hk * H // Hk, (hk + 1) * H // Hk)
+    for lens in ([1, 1], [5, 30], [700, 300]):             # tokens, token by token, chunks of several segments
+        d = make(cuda_dev, lens, dtype, H, Hk, K, V, seed=6, decay=-0.01)
+        for single in ([False, True] if lens == [1, 1] else [False]):
+            out = []
+            for x in (None, bad):
+                s0 = d["s0"].clone()
+                if x is not None:
+                    s0[1, hk, row, col] = x
+                if single:
+                    out.append((ssd.linear_attn_update(s0, d["q"], d["k"], d["v"], d["ld"]), s0))
+                else:
+                    ssd.set_segment_tokens(256)
+                    try:
+                        out.append(ssd.linear_attn_fwd(d["q"], d["k"], d["v"], d["ld"], init_state=s0, cu_seqlens=cu_of(lens, cuda_dev)))
+                    finally:
+                        ssd.set_segment_tokens(0)
+            ssd.device_status()
+            (o, f), (o2, f2) = out
+            assert not bool(torch.isfinite(o2[lens[0]:, hit, row]).any()) and not bool(torch.isfinite(f2[1, hk, row, col]))
+            o2[lens[0]:, hit, row], f2[1, hk, row, col] = o[lens[0]:, hit, row], f[1, hk, row, col]
+            assert torch.equal(o, o2) and torch.equal(f, f2)
