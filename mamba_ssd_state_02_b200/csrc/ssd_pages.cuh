@@ -106,7 +106,7 @@ k_pages_plan(const Meta m, const int32_t* __restrict__ a, const int32_t* __restr
             continue;
         }
         if (OP == COPY) {
-            bad |= x != y && take_bit(bits, y);
+            bad |= take_bit(bits, y);            // a page copied onto itself counts as a destination too
         } else if (OP == FORK) {
             bad |= take_bit(bits, y) || m.length[y] != 0 || !row_ok(m, x);
         } else {

@@ -367,3 +367,18 @@ def test_sequences_branch_finish_and_move(ssd, cuda_dev):
         for layer in layers:
             assert bool(((layer[page].double() - ref["final"][0]).abs() <= 400 * 2.0 ** -23 * ref["s_mag"][0]).all())
     assert not torch.equal(layers[0, int(pool.live[3])], layers[0, int(pool.live[4])])
+
+
+def test_copies_onto_themselves(ssd, cuda_dev):
+    """Page x onto page x moves nothing and counts as a destination: x is no other pair's source
+    or destination."""
+    pool, model = both(ssd, cuda_dev, 8, 6, 2)
+    ssd.pages_copy(pool, ints([3, 0, 5], cuda_dev), ints([3, 1, 5], cuda_dev))
+    ssd.device_status()
+    model.copy([3, 0, 5], [3, 1, 5])
+    model.same(pool)
+    for src, dst in (([3, 0], [3, 3]), ([0, 3], [3, 3]), ([3, 3], [3, 0]), ([3, 3], [3, 3])):
+        ssd.pages_copy(pool, ints(src, cuda_dev), ints(dst, cuda_dev))
+        with pytest.raises(ssd.SSDError, match="INVALID_ARG"):
+            ssd.device_status()
+        model.same(pool)
