@@ -364,7 +364,8 @@ ssd_status ssd_linear_attn_fwd_workspace_size(const ssd_linear_attn_dims* dims, 
  *   init_state and final_state may be the same array (states continue in place); they must
  *   not overlap otherwise, and o overlaps nothing. With a page list, a final page that an earlier sequence writes,
  *   or that another sequence starts from (one array), is not written and latches
- *   SSD_ERR_INVALID_ARG. With page lists both arrays have n_pages states.
+ *   SSD_ERR_INVALID_ARG. An array with a page list has n_pages states, one without nseq; one
+ *   array with one page list has n_pages, and nseq may not be more.
  *   scale: usually 1 / sqrt(K).
  * A NaN or infinity in k or v reaches every output of its sequence and key/value head from
  * the start of its 128-token chunk on (the chunk's products are dense); one in q reaches its

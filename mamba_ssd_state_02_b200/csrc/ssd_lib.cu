@@ -1568,6 +1568,8 @@ extern "C" ssd_status ssd_linear_attn_fwd(const void* q, const void* k, const vo
         return fail(SSD_ERR_INVALID_ARG, "a page list without its states");
     if ((init_pages || final_pages) && (dims->n_pages < 1 || dims->n_pages > INT32_MAX))
         return fail(SSD_ERR_INVALID_ARG, "n_pages must be 1 .. 2^31-1 with a page list");
+    if (init_state == final_state && (init_pages != nullptr) != (final_pages != nullptr) && a.nseq > dims->n_pages)
+        return fail(SSD_ERR_INVALID_ARG, "one array of n_pages states for more sequences than that, with one page list");
     if (a.nseq == 0) {
         t_launches = 0;
         t_last_error.clear();

@@ -185,3 +185,11 @@ def test_token_strides(ssd):
     assert step(row.unflatten(0, (14, 1))) == H * K + 8
     for t in (one.expand(1, 1, H, K), one, torch.zeros(0, H, K), torch.zeros(2, 0, H, K), torch.zeros(3, 7, H, K)):
         assert step(t) == H * K
+
+
+def test_one_array_with_one_page_list_holds_every_sequence(ssd):
+    """The side without a list names states 0 .. nseq-1 of an array of n_pages."""
+    for kw in (dict(ip=P), dict(fp=P)):
+        d = _dims(ssd, lead=(4, 256), n_pages=3)
+        assert _fwd(ssd, d, init=P, fin=P, **kw) == ssd.SSD_ERR_INVALID_ARG
+        assert b"more sequences" in ssd._lib.ssd_last_error()
