@@ -164,6 +164,18 @@ int sm_count() {
     return n;
 }
 
+// Lets `kernel` be launched with `bytes` of dynamic shared memory. The limit belongs to the kernel
+// and not to the call, so it is always set to the same value, all that a block can have beside one KiB
+// of static shared memory: with the call's own size, a thread with smaller dimensions would
+// lower it between another one's setting and launch, and that launch would fail.
+constexpr size_t kMostSmem = 226 * 1024;
+
+template <typename... P>
+cudaError_t allow_smem(void (*kernel)(P...), size_t bytes) {
+    if (bytes > kMostSmem) return cudaErrorInvalidValue;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMostSmem);
+}
+
 // Segment length forced by ssd_set_segment_tokens (0: the planner chooses).
 std::atomic<int> g_segment_override{0};
 // Test hook set by ssd_test_stall: the tensor-core pass whose UMMA warp stalls (0: none).
@@ -1485,7 +1497,7 @@ ssd_status launch_la(const LaPlan& p, const LaMaps& m, int64_t segs, cudaStream_
     static_assert(la::kSimtV == 64 && la::kTcV == 64, "both kernels take 64 columns of V per CTA");
     if (!p.bf16) {
         const size_t smem = la::simt_smem(a.K, OUT);
-        cudaError_t e = cudaFuncSetAttribute(la::k_la_simt<OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        const cudaError_t e = allow_smem(la::k_la_simt<OUT>, smem);
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(linear attention)");
         StageScope sc(OUT ? ST_LA_SCAN : ST_LA_STATE, st);
         la::k_la_simt<OUT><<<grid, la::kSimtThreads, smem, st>>>(a);
@@ -1786,8 +1798,7 @@ template <pages::Op OP>
 ssd_status pages_plan(const PagesWork& w, const int32_t* a, const int32_t* b, int32_t n, int copy_last, cudaStream_t st) {
     const size_t bits = align_up(((size_t)(OP == pages::COPY ? w.m.n_pages : w.m.n_rows) + 31) / 32 * 4, 16);
     if (bits > 40 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(pages::k_pages_plan<OP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (int)bits);
+        const cudaError_t e = allow_smem(pages::k_pages_plan<OP>, bits);
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(pages)");
     }
     StageScope sc(ST_PAGES_PLAN, st);

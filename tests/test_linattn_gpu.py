@@ -717,3 +717,43 @@ def test_a_non_finite_state_stays_in_its_row(ssd, cuda_dev, dtype, bad):
             assert not bool(torch.isfinite(o2[lens[0]:, hit, row]).any()) and not bool(torch.isfinite(f2[1, hk, row, col]))
             o2[lens[0]:, hit, row], f2[1, hk, row, col] = o[lens[0]:, hit, row], f[1, hk, row, col]
             assert torch.equal(o, o2) and torch.equal(f, f2)
+
+
+def at_once(jobs, times):
+    """Every job (a function of the library and its arguments) `times` times in a host thread of
+    its own; how many of them returned an error."""
+    import threading
+    failed, start = [0] * len(jobs), threading.Barrier(len(jobs))
+
+    def loop(i):
+        fn, args = jobs[i]
+        start.wait()
+        failed[i] = sum(fn(*args) != 0 for _ in range(times))
+
+    threads = [threading.Thread(target=loop, args=(i,)) for i in range(len(jobs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    return failed
+
+
+def test_threads_with_other_sizes(ssd, cuda_dev):
+    """Calls of host threads whose kernels take different amounts of shared memory."""
+    import ctypes
+    jobs, checks, keep = [], [], []
+    for K in (128, 16):
+        d = make(cuda_dev, [40], torch.float32, 2, 2, K, 16, seed=K)
+        o, fin = torch.empty(40, 2, 16, device=cuda_dev), torch.empty(1, 2, 16, K, device=cuda_dev)
+        dims, st = ssd.linear_attn_dims((1, 40), 2, 2, K, 16, ssd.SSD_DTYPE_F32), torch.cuda.Stream()
+        jobs.append((ssd._lib.ssd_linear_attn_fwd,
+                     (d["q"].data_ptr(), d["k"].data_ptr(), d["v"].data_ptr(), d["ld"].data_ptr(), 1.0, d["s0"].data_ptr(), None, None,
+                      o.data_ptr(), fin.data_ptr(), None, ctypes.byref(dims), st.cuda_stream)))
+        checks.append((o, fin, LO.linattn(d["q"], d["k"], d["v"], d["ld"], 1.0, d["s0"]), K))
+        keep.append((d, dims, st))
+    torch.cuda.synchronize()
+    assert at_once(jobs, 5000) == [0, 0]
+    ssd.device_status()
+    for o, fin, ref, K in checks:
+        check(o, fin, ref, torch.float32, K, 40)

@@ -382,3 +382,22 @@ def test_copies_onto_themselves(ssd, cuda_dev):
         with pytest.raises(ssd.SSDError, match="INVALID_ARG"):
             ssd.device_status()
         model.same(pool)
+
+
+def test_threads_with_pools_of_other_sizes(ssd, cuda_dev):
+    """Calls of host threads on pools whose requests take different amounts of shared memory (one
+    bit a page: 56 and 128 KiB)."""
+    from test_linattn_gpu import at_once
+    jobs, arrays, keep = [], [], []
+    for n in (458752, 1 << 20):
+        a = torch.arange(n, dtype=torch.int32, device=cuda_dev).view(n, 1)
+        pool, st = ssd.PagePool([a], 2, 2), torch.cuda.Stream()
+        src, dst = ints([n - 1], cuda_dev), ints([0], cuda_dev)
+        jobs.append((ssd._lib.ssd_pages_copy, (pool._ref, src.data_ptr(), dst.data_ptr(), 1, st.cuda_stream)))
+        arrays.append(a)
+        keep.append((pool, st, src, dst))
+    torch.cuda.synchronize()
+    assert at_once(jobs, 5000) == [0, 0]
+    ssd.device_status()
+    for a in arrays:
+        assert int(a[0]) == len(a) - 1 and int(a[1]) == 1
