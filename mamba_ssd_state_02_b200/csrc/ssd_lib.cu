@@ -1109,7 +1109,7 @@ ssd_status launch_strict(const Plan& pl, char* ws, const T* x, const float* dt_r
         case 128: scan_kernel = k_strict_chunk_scan<T, 128>; break;
         default: return fail(SSD_ERR_UNSUPPORTED, "headdim %d", P);
     }
-    cudaError_t e = cudaFuncSetAttribute(scan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)scan_smem);
+    cudaError_t e = allow_smem(scan_kernel, scan_smem);
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(strict chunk scan)");
     int n = 0;
     {
@@ -1133,8 +1133,7 @@ ssd_status launch_strict(const Plan& pl, char* ws, const T* x, const float* dt_r
             const size_t sm = chunk_state_smem<T>(P, N, Q);
             switch (P * N / kThreads) {
 #define SSD_NOUT(V)                                                                                        \
-                case V: if (cudaFuncSetAttribute(k_strict_chunk_state<T, V>,                                  \
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm) != cudaSuccess) \
+                case V: if (allow_smem(k_strict_chunk_state<T, V>, sm) != cudaSuccess)                        \
                         return fail(SSD_ERR_CUDA, "cudaFuncSetAttribute(strict chunk state)");               \
                     k_strict_chunk_state<T, V><<<grid, kThreads, sm, st>>>(x, B, dtc, acum, table, count,     \
                                                                           H, G, P, N, Q, states);            \
@@ -1181,7 +1180,7 @@ ssd_status launch_strict_decode(const Plan& pl, const ssd_chunk_cache& cc, const
     const int H = pl.H, G = pl.G, P = pl.P, N = pl.N, Q = pl.Q;
     const size_t dsm = decode_smem(H, G, N, Q);
     if (dsm > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(k_strict_decode<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dsm);
+        cudaError_t e = allow_smem(k_strict_decode<T>, dsm);
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(strict decode)");
     }
     {
@@ -1200,8 +1199,7 @@ ssd_status launch_strict_decode(const Plan& pl, const ssd_chunk_cache& cc, const
         const unsigned fold_grid = (unsigned)(((int64_t)grid + per_block - 1) / per_block);
         switch (P * N / kThreads) {
 #define SSD_NOUT(V)                                                                                              \
-            case V: if (cudaFuncSetAttribute(k_strict_fold<T, V>, cudaFuncAttributeMaxDynamicSharedMemorySize,   \
-                                             (int)sm) != cudaSuccess)                                           \
+            case V: if (allow_smem(k_strict_fold<T, V>, sm) != cudaSuccess)                                     \
                     return fail(SSD_ERR_CUDA, "cudaFuncSetAttribute(strict fold)");                            \
                 k_strict_fold<T, V><<<fold_grid, kThreads, sm, st>>>(                                           \
                         cc.state, static_cast<const T*>(cc.x), static_cast<const T*>(cc.B), cc.dt, cc.acum, cc.len, \

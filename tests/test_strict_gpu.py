@@ -369,3 +369,26 @@ def test_strict_decode_full_batch_bitwise(ssd, cuda_dev):
                               cu_seqlens=torch.tensor([0, b - a], dtype=torch.int32))
         assert rel_err(got[:, s].cpu(), y_ref[L1[s]:L1[s] + K]) <= TOL_Y[w.dtype]
 
+
+
+def test_threads_with_other_chunks(ssd, cuda_dev):
+    """Decode steps of host threads whose kernels take different amounts of shared memory."""
+    import ctypes
+
+    from test_linattn_gpu import at_once
+    H, P, G, N = 8, 64, 2, 128
+    jobs, keep = [], []
+    for chunk in (256, 64):
+        z = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt, device=cuda_dev)  # noqa: E731
+        cache = ssd.ChunkCache.empty(1, H, P, G, N, chunk, torch.bfloat16, cuda_dev)
+        t = [z(1, H, P), z(1, H, dt=torch.float32), z(H, dt=torch.float32), z(H, dt=torch.float32), z(1, G, N), z(1, G, N),
+             z(H, dt=torch.float32), z(1, H, P)]
+        cc, dims, st = cache._c(), ssd.make_dims(1, H, P, G, N, ssd.SSD_DTYPE_BF16, batch=1, seqlen=1), torch.cuda.Stream()
+        jobs.append((ssd._lib.ssd_strict_state_update,
+                     (ctypes.byref(cc), *[x.data_ptr() for x in t], ctypes.byref(dims), chunk, st.cuda_stream)))
+        keep.append((cache, t, cc, dims, st))
+    torch.cuda.synchronize()
+    assert at_once(jobs, 5000) == [0, 0]
+    ssd.device_status()
+    for (cache, *_), chunk in zip(keep, (256, 64)):
+        assert bool((cache.len == 5000 % chunk).all())
