@@ -757,3 +757,31 @@ def test_threads_with_other_sizes(ssd, cuda_dev):
     ssd.device_status()
     for o, fin, ref, K in checks:
         check(o, fin, ref, torch.float32, K, 40)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("H,Hk,K,V", [(4, 4, 128, 128), (4, 2, 8, 120), (2, 1, 40, 24), (6, 2, 96, 72)])
+@pytest.mark.parametrize("lens,seg", [([700, 333], 0), ([700, 333], 256), ([1500, 130], 1 << 20), ([32, 7], 0)])
+def test_states_and_fp32_outputs_keep_24_bits(ssd, cuda_dev, H, Hk, K, V, dtype, lens, seg):
+    """2-norms over each head: the element bounds above count every rounding at its worst and
+    against sums without cancellation, and would pass a state kept to 16 bits.
+    Tolerance 2^-21 (4.8e-7) of the norm. Inputs of random sign, so that a partial sum of i of n terms
+    is sqrt(i / n) of the whole. Tensor cores: 8 products of 16 tokens a chunk, each truncated, 2^-24 of the
+    partial sum on average and always towards zero: 2^-24 (sqrt(1/8) + .. + sqrt(8/8)) = 3.4e-7.
+    CUDA cores: 64 (chunk) + 128 (scores) roundings of random sign, 2^-24 / sqrt(3) each at most:
+    2^-24 sqrt(32 + 64) / sqrt(3) = 3.4e-7. Powers of lam and the sums over at most 12 chunks or 32 tokens,
+    2^-24 / sqrt(3) each, add sqrt(14 or 32) of that in the square: 2.0e-7. Together below 4.0e-7. Two bf16 terms of
+    w V instead of three would leave 2.7e-6 (2^-8 / sqrt(3) / 1.4, squared)."""
+    for decay in ("mixed", -0.01):
+        d = make(cuda_dev, lens, dtype, H, Hk, K, V, seed=41, decay=decay)
+        ref = LO.linattn(d["q"], d["k"], d["v"], d["ld"], K ** -0.5, d["s0"], lens)
+        ssd.set_segment_tokens(seg)
+        try:
+            o, fin = ssd.linear_attn_fwd(d["q"], d["k"], d["v"], d["ld"], init_state=d["s0"], cu_seqlens=cu_of(lens, cuda_dev))
+        finally:
+            ssd.set_segment_tokens(0)
+        ssd.device_status()
+        rel = lambda x, r, dims: ((x.double() - r).pow(2).sum(dims) / r.pow(2).sum(dims)).sqrt().max().item()  # noqa: E731
+        assert rel(fin, ref["final"], (2, 3)) <= 2.0 ** -21
+        if dtype == torch.float32:
+            assert rel(o, ref["o"], (0, 2)) <= 2.0 ** -21
