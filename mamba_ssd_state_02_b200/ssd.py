@@ -828,7 +828,9 @@ class PagePool:
     views of `meta` (made here, empty, unless given), so one copy of `meta` saves or restores
     them all. `live` holds each row's live page (-1: none), a page list for the linear
     attention calls. Tensors are owned here; the library only reads and writes them. Calls on
-    one pool share its workspace and metadata and must not overlap on the device."""
+    one pool share its workspace and metadata and must not overlap on the device; they may come
+    from any stream, and the pool may be dropped while the last one runs (but not before a graph
+    that was captured with it)."""
 
     def __init__(self, arrays, n_rows, max_pages, meta=None):
         arrays = list(arrays)
@@ -855,6 +857,7 @@ class PagePool:
                         (ctypes.c_int64 * k)(*[t[0].numel() * t.element_size() for t in arrays]),
                         self.refcount.data_ptr(), self.table.data_ptr(), self.length.data_ptr(), self.live.data_ptr())
         self._c, self._ref = c, ctypes.byref(c)
+        self._streams = {_stream(dev)}
         self._reserve(max(n, n_rows))
 
     def _reserve(self, n):
@@ -864,6 +867,19 @@ class PagePool:
         self.workspace = torch.empty(b.value, dtype=torch.uint8, device=self.device)
         self._c.workspace, self._c.workspace_bytes = self.workspace.data_ptr(), b.value
         self._most = n
+
+    def _run(self, fn, *args):
+        if _stream(self.device) not in self._streams:
+            # First call on a stream that the memory does not belong to: torch's allocator must not hand
+            # it out again before this stream is done with it, should the pool be dropped. (While a
+            # graph is captured nothing runs; a pool outlives the graphs that use it.)
+            st = torch.cuda.current_stream(self.device)
+            with torch.cuda.device(self.device):
+                if not torch.cuda.is_current_stream_capturing():
+                    for t in (self.workspace, self.meta, *self.arrays):
+                        t.record_stream(st)
+                    self._streams.add(st.cuda_stream)
+        _run(self.device, fn, self._ref, *args)
 
     def _list(self, t, name, n=None):
         _need(t, name, (t.numel() if n is None else n,), torch.int32, self.device)
@@ -876,7 +892,7 @@ def pages_append(pool: PagePool, rows, copy_last=False):
     """One more (live) page for each listed row, the lowest free ones (ssd_pages_append);
     copy_last: it continues from a copy of the row's last page."""
     n = pool._list(rows, "rows")
-    _run(pool.device, _lib.ssd_pages_append, pool._ref, rows.data_ptr(), n, 1 if copy_last else 0)
+    pool._run(_lib.ssd_pages_append, rows.data_ptr(), n, 1 if copy_last else 0)
 
 
 def pages_fork(pool: PagePool, parents, children):
@@ -884,13 +900,13 @@ def pages_fork(pool: PagePool, parents, children):
     (ssd_pages_fork)."""
     n = pool._list(parents, "parents")
     pool._list(children, "children", n)
-    _run(pool.device, _lib.ssd_pages_fork, pool._ref, parents.data_ptr(), children.data_ptr(), n)
+    pool._run(_lib.ssd_pages_fork, parents.data_ptr(), children.data_ptr(), n)
 
 
 def pages_free(pool: PagePool, rows):
     """Empties the listed rows; pages that no row holds any more are free (ssd_pages_free)."""
     n = pool._list(rows, "rows")
-    _run(pool.device, _lib.ssd_pages_free, pool._ref, rows.data_ptr(), n)
+    pool._run(_lib.ssd_pages_free, rows.data_ptr(), n)
 
 
 def pages_compact(pool: PagePool, remap=None, counts=None):
@@ -901,7 +917,7 @@ def pages_compact(pool: PagePool, remap=None, counts=None):
     counts = torch.empty(2, dtype=torch.int32, device=dev) if counts is None else counts
     _need(remap, "remap", (pool.n_pages,), torch.int32, dev)
     _need(counts, "counts", (2,), torch.int32, dev)
-    _run(dev, _lib.ssd_pages_compact, pool._ref, remap.data_ptr(), counts.data_ptr())
+    pool._run(_lib.ssd_pages_compact, remap.data_ptr(), counts.data_ptr())
     return remap, counts
 
 
@@ -909,4 +925,4 @@ def pages_copy(pool: PagePool, src, dst):
     """Copies the bytes of pages src[i] into pages dst[i] in every array (ssd_pages_copy)."""
     n = pool._list(src, "src")
     pool._list(dst, "dst", n)
-    _run(pool.device, _lib.ssd_pages_copy, pool._ref, src.data_ptr(), dst.data_ptr(), n)
+    pool._run(_lib.ssd_pages_copy, src.data_ptr(), dst.data_ptr(), n)

@@ -401,3 +401,24 @@ def test_threads_with_pools_of_other_sizes(ssd, cuda_dev):
     ssd.device_status()
     for a in arrays:
         assert int(a[0]) == len(a) - 1 and int(a[1]) == 1
+
+
+def test_a_pool_dropped_while_another_stream_uses_it(ssd, cuda_dev):
+    """Its workspace, metadata and arrays are not handed out again before that stream is done."""
+    n = 1 << 20
+    pool = ssd.PagePool([torch.zeros(n, 5, device=cuda_dev)], 2, 2)
+    src, dst = ints([n - 1], cuda_dev), ints([0], cuda_dev)
+    sizes = {t.data_ptr(): t.numel() * t.element_size() for t in (pool.workspace, pool.meta, pool.arrays[0])}
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(2_000_000_000)                   # about a second
+        ssd.pages_copy(pool, src, dst)
+        done = torch.cuda.Event()
+        done.record()
+    del pool
+    fresh = [torch.empty(b, dtype=torch.uint8, device=cuda_dev) for b in sizes.values() for _ in range(2)]
+    assert not done.query()
+    assert not any(p <= t.data_ptr() < p + b for t in fresh for p, b in sizes.items())
+    torch.cuda.synchronize()
+    ssd.device_status()
