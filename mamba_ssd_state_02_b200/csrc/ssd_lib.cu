@@ -56,8 +56,8 @@ ssd_status cuda_fail(cudaError_t e, const char* what) {
 // Per-kernel event timing (ssd_profile_enable / ssd_profile_read).
 enum Stage { ST_TABLE, ST_CUMSUM, ST_CHUNK_STATE, ST_STATE_PASSING, ST_CHUNK_SCAN, ST_STATE_UPDATE,
              ST_CONV, ST_CONV_UPDATE, ST_NORM, ST_STRICT_CUMSUM, ST_STRICT_STATE, ST_STRICT_PASSING,
-             ST_STRICT_SCAN, ST_STRICT_CACHE, ST_STRICT_UPDATE, ST_STRICT_FOLD, ST_LA_STATE, ST_LA_PASSING, ST_LA_SCAN, ST_LA_UPDATE,
-             ST_LA_STEPS,             ST_PAGES_PLAN, ST_PAGES_MOVE, ST_COUNT };
+             ST_STRICT_SCAN, ST_STRICT_CACHE, ST_STRICT_UPDATE, ST_STRICT_FOLD,
+             ST_LA_STATE, ST_LA_PASSING, ST_LA_SCAN, ST_LA_UPDATE, ST_LA_STEPS, ST_PAGES_PLAN, ST_PAGES_MOVE, ST_COUNT };
 const char* const kStageName[ST_COUNT] = {"ssd_chunk_table", "ssd_chunk_cumsum", "ssd_chunk_state",
                                           "ssd_state_passing", "ssd_chunk_scan", "ssd_state_update", "ssd_conv1d", "ssd_conv1d_update",
                                           "ssd_gated_rmsnorm", "ssd_strict_cumsum", "ssd_strict_chunk_state",

@@ -526,35 +526,13 @@ k_la_update(float* __restrict__ state, const T* __restrict__ q, const T* __restr
         float d[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) d[u] = fmaf(s[u].x, qv.x, fmaf(s[u].y, qv.y, fmaf(s[u].z, qv.z, s[u].w * qv.w)));
-        // Sum over the LPR lanes of a group. While more than one row is left per lane, a
-        // lane gives half of its rows to its partner (U, U/2, .. shuffles in all instead
-        // of U per step); then plain butterflies.
-        int n = U, off = LPR / 2, mine = 0;
-#pragma unroll
-        for (int st2 = 0; st2 < 3; ++st2) {
-            if (off >= 1 && n > 1) {
-                const bool up = (c4 & off) != 0;
-#pragma unroll
-                for (int i = 0; i < U / 2; ++i)
-                    if (i < n / 2) {
-                        const float give = up ? d[i] : d[i + n / 2], keep = up ? d[i + n / 2] : d[i];
-                        d[i] = keep + __shfl_xor_sync(0xffffffffu, give, off);
-                    }
-                n /= 2;
-                mine += up ? n : 0;
-                off /= 2;
-            }
-        }
-#pragma unroll
-        for (int w = LPR / 16; w >= 1; w /= 2) d[0] += __shfl_xor_sync(0xffffffffu, d[0], w);
-        // each lane group's lanes with the low bits clear hold rows mine .. mine + n - 1
+        const int mine = sum_rows<LPR>(d, c4);
         if (LPR <= 8 || (c4 & (LPR / 8 - 1)) == 0) {
 #pragma unroll
-            for (int i = 0; i < U; ++i)
-                if (i < n) {
-                    const int row = r0 + (mine + i) * GPW;
-                    if (row < V) ob[(int64_t)r * V + row] = from_f32<T>(scale * d[i]);
-                }
+            for (int i = 0; i < rows_left(LPR); ++i) {
+                const int row = r0 + (mine + i) * GPW;
+                if (row < V) ob[(int64_t)r * V + row] = from_f32<T>(scale * d[i]);
+            }
         }
     }
 }
