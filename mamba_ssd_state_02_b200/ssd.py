@@ -672,12 +672,12 @@ def strict_state_update(cache: ChunkCache, x, dt_raw, dt_bias, A, B, C, D, y=Non
 # ---------------------------------------------------------------------------------
 # Linear attention with a decay for each head. A call for one token takes about as long on the
 # host as on the device, so these bindings switch devices only where they have to.
-def _run(dev, fn, *args):
+def _run(dev, stream, fn, *args):
     if torch.cuda.current_device() == dev.index:
-        status = fn(*args, _stream(dev))
+        status = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
-            status = fn(*args, _stream(dev))
+            status = fn(*args, stream)
     if status != SSD_OK:
         _check(status)
 
@@ -788,7 +788,7 @@ def linear_attn_fwd(q, k, v, log_decay, scale=None, init_state=None, init_pages=
         if need > 256:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
             dims.workspace, dims.workspace_bytes = workspace.data_ptr(), need
-    _run(dev, _lib.ssd_linear_attn_fwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+    _run(dev, _stream(dev), _lib.ssd_linear_attn_fwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
          K ** -0.5 if scale is None else scale, _ptr(init_state), _ptr(init_pages), _ptr(cu_seqlens), o.data_ptr(),
          final_state.data_ptr(), _ptr(final_pages), ctypes.byref(dims))
     return o, final_state
@@ -814,8 +814,8 @@ def linear_attn_update(state, q, k, v, log_decay, scale=None, pages=None, o=None
     else:
         _need(o, "o", (b, H, V), dt, dev)
     dims = linear_attn_dims((b, 1), H, Hk, K, V, _dtype_code(q), None, strides, n_pages)
-    _run(dev, _lib.ssd_linear_attn_update, state.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
-         K ** -0.5 if scale is None else scale, _ptr(pages), o.data_ptr(), ctypes.byref(dims))
+    _run(dev, _stream(dev), _lib.ssd_linear_attn_update, state.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+         log_decay.data_ptr(), K ** -0.5 if scale is None else scale, _ptr(pages), o.data_ptr(), ctypes.byref(dims))
     return o
 
 
@@ -869,17 +869,20 @@ class PagePool:
         self._most = n
 
     def _run(self, fn, *args):
-        if _stream(self.device) not in self._streams:
-            # First call on a stream that the memory does not belong to: torch's allocator must not hand
-            # it out again before this stream is done with it, should the pool be dropped. (While a
-            # graph is captured nothing runs; a pool outlives the graphs that use it.)
-            st = torch.cuda.current_stream(self.device)
-            with torch.cuda.device(self.device):
-                if not torch.cuda.is_current_stream_capturing():
-                    for t in (self.workspace, self.meta, *self.arrays):
-                        t.record_stream(st)
-                    self._streams.add(st.cuda_stream)
-        _run(self.device, fn, self._ref, *args)
+        stream = _stream(self.device)
+        if stream not in self._streams:
+            self._adopt(stream)
+        _run(self.device, stream, fn, self._ref, *args)
+
+    def _adopt(self, stream):
+        """First call on a stream that the memory does not belong to: torch's allocator must not hand
+        it out again before this stream is done with it, should the pool be dropped. (While a graph
+        is captured nothing runs; a pool outlives the graphs that use it.)"""
+        with torch.cuda.device(self.device):
+            if not torch.cuda.is_current_stream_capturing():
+                for t in (self.workspace, self.meta, *self.arrays):
+                    t.record_stream(torch.cuda.current_stream())
+                self._streams.add(stream)
 
     def _list(self, t, name, n=None):
         _need(t, name, (t.numel() if n is None else n,), torch.int32, self.device)
