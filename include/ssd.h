@@ -321,7 +321,8 @@ ssd_status ssd_strict_state_update(const ssd_chunk_cache* cache, const void* x, 
  *
  * Layouts (T tokens in the call, packed like the scan's inputs):
  *   q [T,H,K], k [T,Hk,K], v [T,Hk,V] in `dtype`; heads contiguous, tokens q_stride,
- *     k_stride and v_stride elements apart (0: contiguous), so q, k and v may be slices of
+ *     k_stride and v_stride elements apart (0: contiguous, not one token for all; no fewer than
+ *     a token's heads), so q, k and v may be slices of
  *     one projection's output; every sequence of a dense batch follows the previous one
  *     without a gap, seqlen strides on;
  *   o [T,H,V] in `dtype`, contiguous;  log_decay [Hk] float32, <= 0 and finite (0: no decay);
@@ -395,7 +396,10 @@ ssd_status ssd_linear_attn_update(float* state, const void* q, const void* k, co
  * Pages of a state cache. A pool is a set of device arrays with the same number of pages
  * along their first dimension (page p of array i: page_bytes[i] bytes at arrays[i] +
  * p * page_bytes[i]); one page is one state in every array, for instance the SSM state,
- * conv state and linear attention state of every layer. Metadata, all int32 on the device
+ * conv state and linear attention state of every layer. The linear attention calls read and write
+ * states through page lists; the scan, its decode step and the conv1d take one state per sequence side
+ * by side, so their pages are copied out of the pool (and back) around those calls. Metadata, all
+ * int32 on the device
  * and all zero / -1 for an empty pool (refcount 0, table -1, length 0, live -1):
  *   refcount [n_pages]: rows that hold the page, 0 for a free one;
  *   table [n_rows, max_pages]: the pages of each row (one sequence) in order, -1 past them;

@@ -1335,10 +1335,12 @@ struct LaPlan {
 // Segment length in tokens (a multiple of 128). A pass's CTAs, one per (segment, key/value
 // head, 64 columns of V), run in waves of one per SM; a CTA of the output pass costs its chunks
 // times the query heads plus about five of those units to start and end, one of the state pass
-// 0.6 of a unit a chunk and three to start and end (measured: 2 and 1.2 us, 10 and 5 us). Dense: the number of segments per sequence with the least cost. Packed (lengths known
-// on the device only): the same with the mean length, where the longest segments are what the
-// last wave waits for. The CUDA-core kernel has two CTAs per SM where their shared memory fits,
-// and no state pass for a single segment.
+// 0.6 of a unit a chunk and three to start and end (2 and 1.2 us, 10 and 5 us: a lone call of one
+// chunk takes 17 us. With every SM busy a CTA of one chunk takes 24 and 8 us, which the rule
+// does not count: such calls have no segments to choose). Dense: the number of segments per sequence
+// with the least cost. Packed (lengths known on the device only): the same with the mean length,
+// where the longest segments are what the last wave waits for. The CUDA-core kernel has two CTAs per
+// SM where their shared memory fits, and no state pass for a single segment.
 int la_segment_tokens(const LaPlan& p) {
     constexpr int64_t kC = 128;
     const la::Args& a = p.a;
@@ -1378,9 +1380,10 @@ int la_segment_tokens(const LaPlan& p) {
     return (int)(ls * kC);
 }
 
-// Sequences of up to this many tokens go token by token: 0.45 us a token where the GPU is not full
-// (4 heads of 128 x 128, bf16: 64 tokens 30 us against 16 in chunks, 1 token 3.3 against 15), but
-// 2048 states of 64 tokens take 769 us against 923 (fp32 848 against 723), of fewer tokens less.
+// Sequences of up to this many tokens go token by token. Heads of 128 x 128, bf16, with an initial state:
+// 4 heads (the GPU is not full) 2.9 us for one token, 15 for 32, and 20 for 33 in chunks; 2048 states
+// 402 us for 32 tokens, 856 for 33 in chunks (fp32 428 and 627). Token by token 64 tokens would take
+// 30 us against 20, 769 against 861 (fp32 848 against 719). Other sizes of heads were not measured.
 constexpr int kLaSteps = 32;
 
 ssd_status la_check(const ssd_linear_attn_dims* d, bool varlen, LaPlan* out) {

@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) k_la_simt(const __grid_consta
 // any, and one state serves all R query heads that share it. 256 sequences of 32 heads (1.08 GB
 // of traffic): 165 us, 99% of the measured copy rate. A warp as the unit, each with its own
 // search for pages named twice, was 1.7 times as fast on 16384 rows of 4 KiB states, but took
-// 100 registers instead of 70 and 180 us of the case above. That search is quadratic in the batch:
+// 100 registers instead of 72 and 180 us of the case above. That search is quadratic in the batch:
 // nothing to see at 256 rows, 4 us of 86 at 4096, half of the time at 16384.
 constexpr int kTokThreads = 128;
 constexpr int kTokRows = 8;          // state rows in flight per lane group
@@ -542,10 +542,12 @@ k_la_update(float* __restrict__ state, const T* __restrict__ q, const T* __restr
 // from the sequence's first token to its last, so that it crosses HBM twice however many tokens
 // there are. A warp holds 8 to 64 rows of one state (a lane eight neighbouring rows, four columns) and
 // needs nothing from other warps; the next token's q, k and v are on their way while one is
-// computed. 4 K V FMAs a token where the chunked form has fewer and tensor cores for them, but
-// no CTA of it starts and ends in less than 25 us per 64 columns of V. 256 sequences of one token
-// (32 heads, 128 x 128): 167 us, 99% of the measured copy rate (in chunks 3530 us); of 16 tokens 824 us.
-// Bound by instruction issue from a few tokens on (274 instructions a token and warp, 69% of the
+// computed. 4 K V FMAs a token where the chunked form has fewer and tensor cores for them, but a lone
+// call of one chunk takes 17 us there (both passes; 20 with an initial state), and on a full GPU every
+// CTA (64 columns of V) 8 us of the state pass and 24 of the output pass, however short its
+// sequence. 256 sequences of one token (32 heads, 128 x 128): 167 us, 99% of the measured copy rate (in
+// chunks 3530 us); of 16 tokens 824 us.
+// Bound by instruction issue from a few tokens on (274 instructions a token and warp, 66% of the
 // issue slots). Packed pairs of FMAs and batches of four tokens were no faster.
 template <typename T> struct Raw;                        // elements as they are loaded
 template <> struct Raw<float> {

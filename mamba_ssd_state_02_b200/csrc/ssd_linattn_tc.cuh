@@ -783,6 +783,8 @@ k_la_tc_out(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ C
             S[2 * i + 1] = make_float2(__uint_as_float(x.z), __uint_as_float(x.w));
         }
         if (has_init) named_barrier(1, 32 * kStateWarps);        // read before the operand takes the place
+        // One float of lam^128 is enough here: an error of 2^-25 per chunk that the state remembers, 2^-12
+        // over the longest segment (8192 chunks), beside the 2^-8 of w V's rounding.
         const float2 lam = make_float2(lam_full.x, lam_full.x);
 #pragma unroll 1
         for (int c = has_init ? -1 : 0; c + 1 < nt; ++c) {        // S entering chunk c + 1
