@@ -830,7 +830,7 @@ class PagePool:
     attention calls. Tensors are owned here; the library only reads and writes them. Calls on
     one pool share its workspace and metadata and must not overlap on the device; they may come
     from any stream, and the pool may be dropped while the last one runs (but not before a graph
-    that was captured with it)."""
+    that was captured with it, and not after the end of a stream that was made outside torch)."""
 
     def __init__(self, arrays, n_rows, max_pages, meta=None):
         arrays = list(arrays)
